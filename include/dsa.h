@@ -83,6 +83,9 @@ typedef struct CUstream_st* dsa_stream_t; /* a cudaStream_t */
                                   it while the preceding kernel on the stream finishes        */
 #define DSA_F32 0              /* dsa_index_keys input element types                           */
 #define DSA_BF16 1
+#define DSA_F16 2              /* dsa_rope only                                                */
+#define DSA_ROPE_INTERLEAVED 0x10u /* dsa_rope: pairs (2i, 2i+1) instead of (i, i + pairs)     */
+#define DSA_ROPE_INVERSE 0x20u /* dsa_rope: rotate backwards (the gradient of the rotation)    */
 #define DSA_FILL_MASKED 0x2u   /* dsa_index_scores: write -inf at masked (s > pos) entries of
                                   each row up to S_max (the mask add of Indexer.forward)       */
 
@@ -352,6 +355,102 @@ DSA_API int dsa_sparse_mla_heads(const uint16_t* q, const uint16_t* kv, const in
 DSA_API size_t dsa_sparse_mla_heads_workspace_size(int B, int T, int k, int heads);
 
 /*
+ * Rotary positions for any head layout (the fused calls above rotate only what they transform).
+ *
+ * dsa_rope_freqs - HOST function. Writes the frequencies of `pairs` rotary pairs into the HOST
+ * buffer `freqs`, as fractions of a turn per position in units of 2^-64:
+ * f_i = theta^(-i / pairs) radians, for factor > 1 slowed for long contexts: with original_len > 0
+ * the YaRN blend (pairs that turn more than beta_fast times in original_len positions keep f_i,
+ * those below beta_slow get f_i / factor, linear between, the correction range rounded outwards),
+ * with original_len = 0 every pair gets f_i / factor. theta 1e4, factor 40, original_len 4096,
+ * beta 32 and 1 give the frequencies of dsa_rope_table.
+ * DSA_ERR_INVALID_ARG unless freqs is given, 1 <= pairs <= 2048, theta > 1, factor >= 1,
+ * original_len >= 0 and beta_fast > beta_slow > 0 (all finite).
+ */
+DSA_API int dsa_rope_freqs(uint64_t* freqs, int pairs, double theta, double factor, int original_len,
+                           double beta_fast, double beta_slow);
+
+/*
+ * dsa_rope - out = scale * R(pos * f) x on the features [offset, offset + 2 pairs) of every head,
+ * the other features copied.
+ *
+ *   x, out   [rows][heads][dim] of `dtype` (DSA_F32, DSA_BF16, DSA_F16), features contiguous, rows
+ *            and heads at the given strides (elements, >= 0; out's heads and rows must not overlap).
+ *            out == x with the same strides rotates in place (only the rotary features are then
+ *            touched); otherwise the two must not overlap (not checked here).
+ *   pos      int32 [rows], any value: a negative one turns backwards, so cached keys move from one
+ *            position to another by the difference
+ *   freqs    uint64 [pairs] from dsa_rope_freqs (copied to the device)
+ *   flags    DSA_ROPE_INTERLEAVED: pairs (2i, 2i+1) (the attention's q_pe, k_pe), else (i, i + pairs)
+ *            (the indexer's); DSA_ROPE_INVERSE: turn by -pos, which is the gradient: with g the
+ *            gradient of out, dsa_rope(g, ..., the same scale, DSA_ROPE_INVERSE) is that of x
+ *   scale    a finite factor on the rotated features (YaRN's attention factor), 1 for none
+ * pos * f is exact modulo a turn at any position; sine and cosine are fp32, and the result is
+ * rounded once to dtype. x and out need only the alignment of their elements (16-byte aligned rows
+ * run faster), pos 4 bytes and freqs 8. 1 <= heads <= 4096, 1 <= dim <= 4096, rows = 0 does nothing.
+ */
+DSA_API int dsa_rope(const void* x, int dtype, int64_t rows, int heads, int64_t x_row_stride, int64_t x_head_stride,
+                     int dim, int offset, int pairs, const int32_t* pos, const uint64_t* freqs, float scale,
+                     uint32_t flags, void* out, int64_t out_row_stride, int64_t out_head_stride, dsa_stream_t stream);
+
+/*
+ * dsa_mla_shared - latent attention of a batch whose sequences share a prefix of the cache, over
+ * all keys (no selection). The prefix is stored and read once for the whole batch.
+ *
+ *   q       bf16 [B][T][128][576]  absorbed queries (as dsa_sparse_mla)
+ *   prefix  bf16 [P][576]          latent rows that every query sees (NULL if P = 0)
+ *   kv      bf16 [B][S_max][576]   the sequences' own latent rows (NULL if S_max = 0)
+ *   q_pos   int32 [B][T], kv_len int32 [B]  own rows that query (b, t) sees: s <= q_pos[b][t] and
+ *           s < kv_len[b], counted from the first own row (not from the prefix); clamped to
+ *           [0, S_max]. NULL if S_max = 0.
+ *   out     bf16 [B][T][128][512]; lse fp32 [B][T][128] or NULL (natural log), over prefix and own
+ *   workspace / ws_bytes: at least dsa_mla_shared_workspace_size(B, T, P, S_max) bytes; holds
+ *           nothing between calls, and must not be shared by calls that overlap on the GPU
+ * z = softmax_scale * q . key over the 576 features of the visible rows, out = softmax(z) . key[0:512].
+ * A query that sees no row gets zeros and lse = -inf. Own rows that no query of their sequence
+ * sees may hold anything, NaN included. (Among the queries of one sequence, a NaN or infinity in
+ * a row that only the later of two adjacent queries sees may show in the earlier one's output too;
+ * another sequence never sees it.)
+ * P + S_max >= 1; B * T <= 2^23; P and S_max at most DSA_MAX_POS; pointers 16-byte aligned.
+ */
+DSA_API int dsa_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const uint16_t* kv,
+                           const int32_t* q_pos, const int32_t* kv_len, int B, int T, int S_max, float softmax_scale,
+                           uint16_t* out, float* lse, void* workspace, size_t ws_bytes, dsa_stream_t stream);
+
+/* Bytes of device scratch dsa_mla_shared needs on the current device (0 for an invalid shape). */
+DSA_API size_t dsa_mla_shared_workspace_size(int B, int T, int P, int S_max);
+
+/*
+ * dsa_cache_evict - cuts every sequence's cache back to at most `keep` rows, by the attention
+ * weight that its rows have collected (dsa_mla_weights), in place.
+ *
+ *   acc     fp32 [B][S_max]   collected weight of each row
+ *   pos     int32 [B][S_max]  position of each row's token (a row keeps it wherever it moves)
+ *   kv_len  int32 [B]         rows present, clamped to [0, S_max]
+ *   keep    rows to keep, >= 1;  recent, sinks >= 0: rows whose position is among the `recent`
+ *           newest (above the sequence's largest position - recent) or below `sinks` are protected
+ *   kv bf16 [B][S_max][576], k8 uint8 [B][S_max][128], k_scale fp32 [B][S_max]: the caches whose
+ *           rows move (each may be NULL; k8 and k_scale go together)
+ *   acc_out, pos_out [B][S_max], kv_len_out [B]: the new state; each may be the input itself
+ *   src     int32 [B][keep] or NULL: the row that each row of the new cache was before, -1 behind it
+ *   workspace / ws_bytes: at least dsa_cache_evict_workspace_size(B, S_max, keep) bytes
+ * A sequence of n <= keep rows stays as it is. Otherwise the first `keep` rows in the order
+ * (protected, larger weight, lower row) stay: those below row `keep` where they are, and the i-th
+ * kept row from `keep` on moves into the i-th given-up row below it. So rows do not stay in the
+ * order of their positions; attention does not depend on it, as every later query sees all of them.
+ * -0 and +0 are equal, and NaN comes below every weight. Rows from the new length on are left as
+ * they were. Outputs that are not their inputs must not overlap them (not checked).
+ * 1 <= B <= 65535; S_max at most DSA_MAX_POS; pointers 16-byte aligned.
+ */
+DSA_API int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* kv_len, int B, int S_max, int keep,
+                            int recent, int sinks, uint16_t* kv, uint8_t* k8, float* k_scale, float* acc_out,
+                            int32_t* pos_out, int32_t* kv_len_out, int32_t* src, void* workspace, size_t ws_bytes,
+                            dsa_stream_t stream);
+
+/* Bytes of device scratch dsa_cache_evict needs (0 for an invalid shape). */
+DSA_API size_t dsa_cache_evict_workspace_size(int B, int S_max, int keep);
+
+/*
  * dsa_get_device_status - synchronises `stream`, returns the first error recorded by a kernel
  * since the last call (DSA_OK if none) and clears it. DSA_ERR_CUDA if the sync itself fails.
  */
@@ -381,6 +480,12 @@ DSA_API int dsa_get_device_status(dsa_stream_t stream);
 #define DSA_SITE_ABSORB_A_EMPTY 0x43    /* MLA absorption: TMA waits for a free stage            */
 #define DSA_SITE_ABSORB_ACC_FULL 0x44   /* MLA absorption: epilogue waits for an accumulator     */
 #define DSA_SITE_ABSORB_ACC_EMPTY 0x45  /* MLA absorption: MMA waits for a drained accumulator   */
+#define DSA_SITE_SHARED_Q 0x51          /* shared prefix: MMA waits for the queries (TMA)        */
+#define DSA_SITE_SHARED_FULL 0x52       /* shared prefix: MMA waits for a block of keys          */
+#define DSA_SITE_SHARED_EMPTY 0x53      /* shared prefix: loads wait for free shared memory      */
+#define DSA_SITE_SHARED_S 0x54          /* shared prefix: softmax waits for a score tile         */
+#define DSA_SITE_SHARED_P 0x55          /* shared prefix: MMA waits for probabilities            */
+#define DSA_SITE_SHARED_O 0x56          /* shared prefix: output waits for P V, or P V for it    */
 
 /*
  * dsa_get_error_detail - the detail recorded with the last non-OK code that

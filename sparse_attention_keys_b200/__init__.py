@@ -7,6 +7,7 @@ the library's CUDA kernels; there is no fallback path. Names follow the C entry 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -18,7 +19,8 @@ __all__ = [
     "dsa_index_topk", "dsa_sparse_mla", "dsa_sparse_mla_workspace_size", "dsa_sparse_mla_noalloc", "dsa_sparse_mla_heads",
     "dsa_sparse_mla_heads_workspace_size",
     "dsa_index_scores_paged", "dsa_sparse_mla_paged", "dsa_mla_q_absorb", "dsa_mla_kv_entry",
-    "dsa_mla_out_absorb",
+    "dsa_mla_out_absorb", "dsa_rope_freqs", "dsa_rope", "dsa_mla_shared", "dsa_mla_shared_workspace_size",
+    "dsa_cache_evict", "dsa_cache_evict_workspace_size", "DSA_F16", "DSA_ROPE_INTERLEAVED", "DSA_ROPE_INVERSE",
     "dsa_sparse_mla_noalloc_scratch_bytes", "dsa_get_device_status", "dsa_get_error_detail",
     "dsa_selftest_wait_timeout", "dsa_status_string", "dsa_device_supported", "dsa_version",
     "SITE_NAMES",
@@ -31,6 +33,9 @@ DSA_SORTED = 0x4
 DSA_Q_READY = 0x8
 DSA_F32 = 0
 DSA_BF16 = 1
+DSA_F16 = 2
+DSA_ROPE_INTERLEAVED = 0x10
+DSA_ROPE_INVERSE = 0x20
 MAX_POS = 16384                 # max_seq_len of the model (ModelArgs)
 INDEXER_SOFTMAX_SCALE = 128 ** -0.5
 MLA_SOFTMAX_SCALE = 192 ** -0.5 * (1.0 + 0.1 * __import__("math").log(40.0)) ** 2
@@ -42,6 +47,7 @@ SITE_NAMES = {
     0x24: "mla:s_full", 0x25: "mla:p_full", 0x26: "mla:p_empty", 0x27: "mla:o_full",
     0x31: "selftest", 0x41: "absorb:w", 0x42: "absorb:a_full", 0x43: "absorb:a_empty",
     0x44: "absorb:acc_full", 0x45: "absorb:acc_empty",
+    0x51: "shared:q", 0x52: "shared:full", 0x53: "shared:empty", 0x54: "shared:s", 0x55: "shared:p", 0x56: "shared:o",
 }
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -79,6 +85,15 @@ def _load():
     L.dsa_mla_kv_entry.argtypes = [vp, vp, vp, vp, i32, i64, vp, vp, i64, vp]
     L.dsa_mla_out_absorb.argtypes = [vp, vp, i64, i64, vp, vp]
     L.dsa_sparse_mla_workspace_size.restype = sz
+    f64 = ctypes.c_double
+    L.dsa_rope_freqs.argtypes = [vp, i32, f64, f64, i32, f64, f64]
+    L.dsa_rope.argtypes = [vp, i32, i64, i32, i64, i64, i32, i32, i32, vp, vp, f32, u32, vp, i64, i64, vp]
+    L.dsa_mla_shared.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+    L.dsa_mla_shared_workspace_size.argtypes = [i32, i32, i32, i32]
+    L.dsa_mla_shared_workspace_size.restype = sz
+    L.dsa_cache_evict.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.dsa_cache_evict_workspace_size.argtypes = [i32, i32, i32]
+    L.dsa_cache_evict_workspace_size.restype = sz
     L.dsa_sparse_mla_noalloc.argtypes = [vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp]
     L.dsa_sparse_mla_noalloc_scratch_bytes.argtypes = []
     L.dsa_sparse_mla_noalloc_scratch_bytes.restype = sz
@@ -93,7 +108,8 @@ def _load():
               "dsa_sparse_mla_ex",
               "dsa_sparse_mla_heads",
               "dsa_sparse_mla_noalloc", "dsa_get_device_status", "dsa_get_error_detail",
-              "dsa_selftest_wait_timeout", "dsa_device_supported"):
+              "dsa_selftest_wait_timeout", "dsa_device_supported", "dsa_rope_freqs", "dsa_rope", "dsa_mla_shared",
+              "dsa_cache_evict"):
         getattr(L, f).restype = ctypes.c_int
     return L
 
@@ -503,6 +519,205 @@ def dsa_mla_out_absorb(o, w_uv, out=None, stream=None):
     rc = _lib.dsa_mla_out_absorb(_ptr(o), _ptr(w), ws, rows, _ptr(out), _stream(stream))
     _check(rc, "dsa_mla_out_absorb")
     return out
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Makes `device` current and yields the stream to launch on (its current one by default). What is
+    allocated inside belongs to that stream, so it is not handed out again before its work is done."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield _stream(torch.cuda.current_stream())
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+            with torch.cuda.stream(stream):
+                yield _stream(stream)
+
+
+def _one_device(first, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{n} is on {t.device}, not on {first.device}: all tensors must be on one device")
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _scratch(workspace, size, device):
+    """The caller's workspace as (tensor, bytes), or a fresh one of `size` bytes."""
+    if workspace is None:
+        workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    _need(workspace, workspace.dtype, "workspace")
+    if workspace.device != device:
+        raise ValueError("workspace must be on the tensors' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def dsa_rope_freqs(pairs: int, theta: float = 10000.0, factor: float = 1.0, original_len: int = 0,
+                   beta_fast: float = 32.0, beta_slow: float = 1.0) -> torch.Tensor:
+    """Rotary frequencies as int64 [pairs] (fractions of a turn in units of 2^-64) in HOST memory. factor > 1
+    slows them for long contexts: by YaRN with original_len > 0, all alike with original_len = 0."""
+    if int(pairs) < 1:
+        raise ValueError("pairs must be at least 1")
+    out = torch.empty(int(pairs), dtype=torch.int64)
+    _check(_lib.dsa_rope_freqs(_ptr(out), int(pairs), float(theta), float(factor), int(original_len), float(beta_fast),
+                               float(beta_slow)), "dsa_rope_freqs")
+    return out
+
+
+def dsa_rope(x, pos, freqs, offset: int = 0, interleaved: bool = False, inverse: bool = False, scale: float = 1.0,
+             out=None, stream=None):
+    """x fp32, bf16 or fp16 [rows, heads, dim] or [rows, dim], features contiguous, rows and heads at any stride;
+    pos i32 [rows]; freqs i64 [pairs] from dsa_rope_freqs, on the device. Rotates the features
+    [offset, offset + 2 pairs) of each head as pairs (2i, 2i+1) if interleaved, else (i, i + pairs), and copies the
+    others into `out` (new and contiguous by default; out=x rotates in place). inverse=True with the same scale is the
+    gradient with respect to x."""
+    dtypes = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16, torch.float16: DSA_F16}
+    if not isinstance(x, torch.Tensor) or x.dtype not in dtypes:
+        raise TypeError("x must be a float32, bfloat16 or float16 tensor")
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dim() not in (2, 3):
+        raise ValueError(f"x must be [rows, heads, dim] or [rows, dim], got {list(x.shape)}")
+    _need(pos, torch.int32, "pos")
+    _need(freqs, torch.int64, "freqs")
+    rows, dim, pairs = x.shape[0], x.shape[-1], freqs.numel()
+    heads = x.shape[1] if x.dim() == 3 else 1
+    _shape(pos, (rows,), "pos")
+    if pairs < 1 or offset < 0 or offset + 2 * pairs > dim:
+        raise ValueError(f"features [{offset}, {offset + 2 * pairs}) do not lie in a head of {dim}")
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.dtype != x.dtype:
+            raise TypeError(f"out must be a {x.dtype} tensor")
+        _shape(out, x.shape, "out")
+    _one_device(x, pos=pos, freqs=freqs, out=out)
+    with _on(x.device, stream) as s:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        for t, n in ((x, "x"), (out, "out")):
+            if dim > 1 and t.stride(-1) != 1:
+                raise ValueError(f"the features of {n} must be contiguous")
+        if rows == 0 or heads == 0:
+            return out
+        strides = [(t.stride(0) if rows > 1 else heads * dim, t.stride(1) if t.dim() == 3 and heads > 1 else dim)
+                   for t in (x, out)]
+        if out.data_ptr() != x.data_ptr() or strides[0] != strides[1]:
+            spans = [(t.data_ptr(), t.data_ptr() + t.element_size() * ((rows - 1) * r + (heads - 1) * h + dim))
+                     for t, (r, h) in zip((x, out), strides)]
+            if spans[0][0] < spans[1][1] and spans[1][0] < spans[0][1] and not _interleave(x, out, strides, heads, dim):
+                raise ValueError("out must be x itself or not overlap it")
+        flags = (DSA_ROPE_INTERLEAVED if interleaved else 0) | (DSA_ROPE_INVERSE if inverse else 0)
+        rc = _lib.dsa_rope(_ptr(x), dtypes[x.dtype], rows, heads, strides[0][0], strides[0][1], dim, int(offset), pairs,
+                           _ptr(pos), _ptr(freqs), float(scale), flags, _ptr(out), strides[1][0], strides[1][1], s)
+    _check(rc, "dsa_rope")
+    return out
+
+
+def _interleave(x, out, strides, heads, dim):
+    """Whether two tensors whose memory spans meet are disjoint columns of rows of one stride."""
+    (xr, xh), (outr, outh) = strides
+    if xr != outr:
+        return False
+    gap = (out.data_ptr() - x.data_ptr()) // x.element_size() % xr if xr else 0
+    width_x, width_out = (heads - 1) * xh + dim, (heads - 1) * outh + dim
+    return gap >= width_x and gap + width_out <= xr
+
+
+def dsa_mla_shared_workspace_size(B: int, T: int, P: int, S_max: int) -> int:
+    """Bytes of scratch dsa_mla_shared needs on the current device."""
+    return int(_lib.dsa_mla_shared_workspace_size(int(B), int(T), int(P), int(S_max)))
+
+
+def dsa_mla_shared(q, prefix, kv=None, q_pos=None, kv_len=None, softmax_scale: float = MLA_SOFTMAX_SCALE, out=None,
+                   lse=None, workspace=None, want_lse: bool = True, stream=None):
+    """Dense latent attention over a prefix that the whole batch shares and each sequence's own rows: q bf16
+    [B,T,128,576], prefix bf16 [P,576] (or None), kv bf16 [B,S,576] with q_pos i32 [B,T] and kv_len i32 [B] (or all
+    None): query (b, t) sees the prefix and the own rows s <= q_pos[b,t], s < kv_len[b] -> (out bf16 [B,T,128,512],
+    lse fp32 [B,T,128])."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 4 or tuple(q.shape[2:]) != (128, 576):
+        raise ValueError(f"q must be [B, T, 128, 576], got {list(q.shape)}")
+    B, T = q.shape[:2]
+    P = S = 0
+    if prefix is not None:
+        _need(prefix, torch.bfloat16, "prefix")
+        P = prefix.shape[0]
+        _shape(prefix, (P, 576), "prefix")
+    if kv is not None:
+        _need(kv, torch.bfloat16, "kv")
+        if kv.dim() != 3:
+            raise ValueError(f"kv must be [B, S_max, 576], got {list(kv.shape)}")
+        S = kv.shape[1]
+        _shape(kv, (B, S, 576), "kv")
+        for t, n, shape in ((q_pos, "q_pos", (B, T)), (kv_len, "kv_len", (B,))):
+            _need(t, torch.int32, n)
+            _shape(t, shape, n)
+    elif q_pos is not None or kv_len is not None:
+        raise ValueError("q_pos and kv_len count own rows: they need kv")
+    for t, n, dt, shape in ((out, "out", torch.bfloat16, (B, T, 128, 512)), (lse, "lse", torch.float32, (B, T, 128))):
+        if t is not None:
+            _need(t, dt, n)
+            _shape(t, shape, n)
+    _one_device(q, prefix=prefix, kv=kv, q_pos=q_pos, kv_len=kv_len, out=out, lse=lse)
+    with _on(q.device, stream) as s:
+        if out is None:
+            out = torch.empty((B, T, 128, 512), dtype=torch.bfloat16, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((B, T, 128), dtype=torch.float32, device=q.device)
+        workspace, ws_len = _scratch(workspace, dsa_mla_shared_workspace_size(B, T, P, S), q.device)
+        rc = _lib.dsa_mla_shared(_ptr(q), _ptr(prefix), P, _ptr(kv), _ptr(q_pos), _ptr(kv_len), B, T, S,
+                                 float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_len, s)
+    _check(rc, "dsa_mla_shared")
+    return out, lse
+
+
+def dsa_cache_evict_workspace_size(B: int, S_max: int, keep: int) -> int:
+    return int(_lib.dsa_cache_evict_workspace_size(int(B), int(S_max), int(keep)))
+
+
+def dsa_cache_evict(acc, pos, kv_len, keep: int, recent: int = 0, sinks: int = 0, kv=None, k8=None, k_scale=None,
+                    acc_out=None, pos_out=None, kv_len_out=None, src=None, workspace=None, stream=None):
+    """Cuts each sequence's cache back to `keep` rows by collected weight, in place: acc fp32 [B,S], pos i32 [B,S],
+    kv_len i32 [B]; rows among the `recent` newest positions or below position `sinks` are protected. Moves the rows of
+    the caches given (kv bf16 [B,S,576], k8 u8 [B,S,128] with k_scale fp32 [B,S]); acc, pos and kv_len are updated in
+    place unless acc_out, pos_out, kv_len_out are given. Returns (acc, pos, kv_len, src), src i32 [B,keep] naming the
+    row that each kept row came from (-1 behind them)."""
+    _need(acc, torch.float32, "acc")
+    if acc.dim() != 2:
+        raise ValueError(f"acc must be [B, S_max], got {list(acc.shape)}")
+    B, S = acc.shape
+    keep = int(keep)
+    if keep < 1:
+        raise ValueError("keep must be at least 1")
+    if (k8 is None) != (k_scale is None):
+        raise ValueError("k8 and k_scale go together")
+    acc_out = acc if acc_out is None else acc_out
+    pos_out = pos if pos_out is None else pos_out
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
+    for t, n, dt, shape in ((pos, "pos", torch.int32, (B, S)), (kv_len, "kv_len", torch.int32, (B,)),
+                            (acc_out, "acc_out", torch.float32, (B, S)), (pos_out, "pos_out", torch.int32, (B, S)),
+                            (kv_len_out, "kv_len_out", torch.int32, (B,)), (kv, "kv", torch.bfloat16, (B, S, 576)),
+                            (k8, "k8", torch.uint8, (B, S, 128)), (k_scale, "k_scale", torch.float32, (B, S)),
+                            (src, "src", torch.int32, (B, keep))):
+        if t is not None or n in ("pos", "kv_len"):
+            _need(t, dt, n)
+            _shape(t, shape, n)
+    _one_device(acc, pos=pos, kv_len=kv_len, acc_out=acc_out, pos_out=pos_out, kv_len_out=kv_len_out, kv=kv, k8=k8,
+                k_scale=k_scale, src=src)
+    with _on(acc.device, stream) as s:
+        if src is None:
+            src = torch.empty((B, keep), dtype=torch.int32, device=acc.device)
+        workspace, ws_len = _scratch(workspace, dsa_cache_evict_workspace_size(B, S, keep), acc.device)
+        rc = _lib.dsa_cache_evict(_ptr(acc), _ptr(pos), _ptr(kv_len), B, S, keep, int(recent), int(sinks), _ptr(kv),
+                                  _ptr(k8), _ptr(k_scale), _ptr(acc_out), _ptr(pos_out), _ptr(kv_len_out), _ptr(src),
+                                  _ptr(workspace), ws_len, s)
+    _check(rc, "dsa_cache_evict")
+    return acc_out, pos_out, kv_len_out, src
 
 
 def dsa_sparse_mla_noalloc_scratch_bytes() -> int:

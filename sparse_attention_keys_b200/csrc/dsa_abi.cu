@@ -504,6 +504,112 @@ int dsa_sparse_mla_paged(const uint16_t* q, const uint16_t* kv_pool, int64_t num
                                       softmax_scale, out, lse, workspace, ws_bytes, (cudaStream_t)stream, status);
 }
 
+static bool finite_ge(double v, double least) { return isfinite(v) && v >= least; }
+
+int dsa_rope_freqs(uint64_t* freqs, int pairs, double theta, double factor, int original_len, double beta_fast,
+                   double beta_slow) {
+  if (!freqs || pairs < 1 || pairs > 2048 || !finite_ge(theta, 1.0) || theta == 1.0 || !finite_ge(factor, 1.0) ||
+      original_len < 0 || !finite_ge(beta_slow, 0.0) || beta_slow == 0.0 || !finite_ge(beta_fast, beta_slow) ||
+      beta_fast == beta_slow)
+    return DSA_ERR_INVALID_ARG;
+  const int dim = 2 * pairs;
+  double low = 0, high = 0;
+  if (original_len > 0) {
+    low = std::max(floor(yarn_correction_dim(beta_fast, dim, theta, original_len)), 0.0);
+    high = std::min(ceil(yarn_correction_dim(beta_slow, dim, theta, original_len)), (double)(dim - 1));
+    if (high <= low) high = low + 0.001;
+  }
+  for (int i = 0; i < pairs; ++i) {
+    const long double f = powl((long double)theta, -2.0L * i / dim);
+    long double slowed = 1.0L;                       // the share of the slowed frequency
+    if (original_len > 0) slowed = std::min(std::max(((long double)i - low) / ((long double)high - low), 0.0L), 1.0L);
+    const long double g = factor > 1.0 ? f * (1.0L - slowed) + f / (long double)factor * slowed : f;
+    freqs[i] = (uint64_t)roundl(g / (2.0L * acosl(-1.0L)) * 18446744073709551616.0L);
+  }
+  return DSA_OK;
+}
+
+int dsa_rope(const void* x, int dtype, int64_t rows, int heads, int64_t x_row_stride, int64_t x_head_stride, int dim,
+             int offset, int pairs, const int32_t* pos, const uint64_t* freqs, float scale, uint32_t flags, void* out,
+             int64_t out_row_stride, int64_t out_head_stride, dsa_stream_t stream) {
+  if (dtype != DSA_F32 && dtype != DSA_BF16 && dtype != DSA_F16) return DSA_ERR_INVALID_ARG;
+  if (rows < 0 || rows > 0x7fffffffLL || heads < 1 || heads > 4096 || dim < 1 || dim > 4096 || offset < 0 || pairs < 1 ||
+      (int64_t)offset + 2 * (int64_t)pairs > dim || !isfinite(scale) ||
+      (flags & ~(DSA_ROPE_INTERLEAVED | DSA_ROPE_INVERSE)) != 0)
+    return DSA_ERR_INVALID_ARG;
+  const int64_t limit = (int64_t)1 << 40;
+  if (x_row_stride < 0 || x_row_stride > limit || x_head_stride < 0 || x_head_stride > limit || out_row_stride < 0 ||
+      out_row_stride > limit || out_head_stride < 0 || out_head_stride > limit)
+    return DSA_ERR_INVALID_ARG;
+  if (rows == 0) return DSA_OK;
+  if (!x || !pos || !freqs || !out) return DSA_ERR_INVALID_ARG;
+  const uintptr_t size = dtype == DSA_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % size || reinterpret_cast<uintptr_t>(out) % size ||
+      reinterpret_cast<uintptr_t>(pos) % 4 || reinterpret_cast<uintptr_t>(freqs) % 8)
+    return DSA_ERR_INVALID_ARG;
+  if (out == x && (x_row_stride != out_row_stride || x_head_stride != out_head_stride)) return DSA_ERR_INVALID_ARG;
+  // heads inside a row's stride, or rows inside a head's: no two elements of out coincide
+  const bool rows_outer = (heads == 1 || out_head_stride >= dim) &&
+                          (rows == 1 || out_row_stride >= (heads - 1) * out_head_stride + dim);
+  const bool heads_outer = (rows == 1 || out_row_stride >= dim) &&
+                           (heads == 1 || out_head_stride >= (rows - 1) * out_row_stride + dim);
+  if (!rows_outer && !heads_outer) return DSA_ERR_INVALID_ARG;
+  int* status;
+  int rc = prologue(&status);
+  if (rc != DSA_OK) return rc;
+  return dsa::launch_rope(x, dtype, rows, heads, x_row_stride, x_head_stride, dim, offset, pairs, pos, freqs, scale,
+                          (flags & DSA_ROPE_INTERLEAVED) != 0, (flags & DSA_ROPE_INVERSE) != 0, out, out_row_stride,
+                          out_head_stride, (cudaStream_t)stream);
+}
+
+static bool shared_shape_ok(int B, int T, int P, int S_max) {
+  return B >= 1 && T >= 1 && P >= 0 && P <= DSA_MAX_POS && S_max >= 0 && S_max <= DSA_MAX_POS && P + S_max >= 1 &&
+         (int64_t)B * T <= (1 << 23);
+}
+
+size_t dsa_mla_shared_workspace_size(int B, int T, int P, int S_max) {
+  return shared_shape_ok(B, T, P, S_max) ? dsa::mla_shared_workspace_size(B, T, P, S_max) : 0;
+}
+
+int dsa_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const uint16_t* kv, const int32_t* q_pos,
+                   const int32_t* kv_len, int B, int T, int S_max, float softmax_scale, uint16_t* out, float* lse,
+                   void* workspace, size_t ws_bytes, dsa_stream_t stream) {
+  if (!shared_shape_ok(B, T, P, S_max) || !(softmax_scale > 0.f) || !isfinite(softmax_scale)) return DSA_ERR_INVALID_ARG;
+  if (!q || !out || (P > 0 && !prefix) || (S_max > 0 && (!kv || !q_pos || !kv_len))) return DSA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, prefix, kv, q_pos, kv_len, out, lse, workspace};
+  for (const void* p : ptrs)
+    if (!dsa_host::aligned16(p)) return DSA_ERR_INVALID_ARG;
+  int* status;
+  int rc = prologue(&status);
+  if (rc != DSA_OK) return rc;
+  return dsa::launch_mla_shared(q, prefix, P, kv, q_pos, kv_len, B, T, S_max, softmax_scale, out, lse, workspace,
+                                ws_bytes, (cudaStream_t)stream, status);
+}
+
+static bool evict_shape_ok(int B, int S_max, int keep) {
+  return B >= 1 && B <= 65535 && S_max >= 1 && S_max <= DSA_MAX_POS && keep >= 1;
+}
+
+size_t dsa_cache_evict_workspace_size(int B, int S_max, int keep) {
+  return evict_shape_ok(B, S_max, keep) ? dsa::cache_evict_workspace_size(B, S_max, keep) : 0;
+}
+
+int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* kv_len, int B, int S_max, int keep, int recent,
+                    int sinks, uint16_t* kv, uint8_t* k8, float* k_scale, float* acc_out, int32_t* pos_out,
+                    int32_t* kv_len_out, int32_t* src, void* workspace, size_t ws_bytes, dsa_stream_t stream) {
+  if (!evict_shape_ok(B, S_max, keep) || recent < 0 || sinks < 0) return DSA_ERR_INVALID_ARG;
+  if (!acc || !pos || !kv_len || !acc_out || !pos_out || !kv_len_out || (k8 == nullptr) != (k_scale == nullptr))
+    return DSA_ERR_INVALID_ARG;
+  const void* ptrs[] = {acc, pos, kv_len, kv, k8, k_scale, acc_out, pos_out, kv_len_out, src, workspace};
+  for (const void* p : ptrs)
+    if (!dsa_host::aligned16(p)) return DSA_ERR_INVALID_ARG;
+  int* status;
+  int rc = prologue(&status);
+  if (rc != DSA_OK) return rc;
+  return dsa::launch_cache_evict(acc, pos, kv_len, B, S_max, keep, recent, sinks, kv, k8, k_scale, acc_out, pos_out,
+                                 kv_len_out, src, workspace, ws_bytes, (cudaStream_t)stream);
+}
+
 int dsa_get_device_status(dsa_stream_t stream) {
   DeviceCache* c = device_cache();
   if (!c) return DSA_ERR_CUDA;

@@ -51,4 +51,19 @@ int launch_sparse_mla(const uint16_t* q, const uint16_t* kv, const int32_t* idx,
                       int S_max, int k, int heads, float softmax_scale, uint16_t* out, float* lse,
                       void* workspace, size_t ws_bytes, bool q_ready, cudaStream_t stream, int* status);
 
+// strides in elements; out == x rotates in place
+int launch_rope(const void* x, int dtype, int64_t rows, int heads, int64_t x_row, int64_t x_head, int dim, int offset,
+                int pairs, const int32_t* pos, const uint64_t* freqs, float scale, bool interleaved, bool inverse, void* out,
+                int64_t out_row, int64_t out_head, cudaStream_t stream);
+
+size_t mla_shared_workspace_size(int B, int T, int P, int S_max);
+int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const uint16_t* kv, const int32_t* q_pos,
+                      const int32_t* kv_len, int B, int T, int S_max, float softmax_scale, uint16_t* out, float* lse,
+                      void* workspace, size_t ws_bytes, cudaStream_t stream, int* status);
+
+size_t cache_evict_workspace_size(int B, int S_max, int keep);
+int launch_cache_evict(const float* acc, const int32_t* pos, const int32_t* kv_len, int B, int S_max, int keep, int recent,
+                       int sinks, uint16_t* kv, uint8_t* k8, float* k_scale, float* acc_out, int32_t* pos_out,
+                       int32_t* kv_len_out, int32_t* src, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
 }  // namespace dsa

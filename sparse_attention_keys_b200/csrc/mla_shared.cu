@@ -1,0 +1,723 @@
+// dsa_mla_shared: dense latent attention of a batch whose sequences share a prefix of the cache.
+//
+// For query (b, t) and head h the visible keys are the P rows of the prefix and the first vis rows
+// of sequence b's own cache (vis = min(q_pos + 1, kv_len)): z = scale * q . key over 576 features,
+// out = softmax(z) . key[0:512], lse = ln sum e^z. The prefix is stored once and its tiles are
+// multiplied with the queries of every sequence, so its part is a matrix product with B*T*128 rows.
+//
+// Work. Two tokens (256 rows of q) form a unit; a CTA pair (cta_group::2, M = 256, one token per
+// CTA) accumulates one half (256 features) of the unit's output, since 128 x 512 fp32 would fill
+// the whole TMEM and leave none for the scores. So the scores are computed by both halves: 832
+// instead of 544 multiply-adds per (row, key, CTA pair), the price of keeping O in TMEM. A unit's
+// keys are the prefix, then the own rows of its token(s), in tiles of 128, all accumulated into one
+// O with a running maximum and sum. The tiles of all (unit, half) items in a row are cut into equal
+// ranges, one per CTA pair; an item that a cut divides leaves fp32 partials in the workspace, which
+// a second kernel joins. Every pair holds at most two such pieces, so the workspace is bounded
+// whatever the lengths are, and the device alone reads the lengths.
+//
+// Per CTA: Q (128 x 576, 144 KB) stays in shared memory; K and V stream through one ring of 8 KB
+// blocks in the order the MMAs consume them (K: 64 keys x 64 features, this CTA's half of the
+// tile's keys; V: 32 keys x 128 features, its half of the 256 output features). TMEM: O [0, 256),
+// two score buffers of 128 columns; the probabilities (bf16) replace the scores they came from and
+// are the A operand of P V. Q K^T of tile j + 1 runs while the softmax of tile j does.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "pair.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kHeads = 128;
+constexpr int kDqk = 576, kDv = 512;
+constexpr int kTile = 128;                         // keys per tile
+constexpr int kQBlock = kHeads * 128;              // 16 KB: 64 features of 128 rows
+constexpr int kQBytes = 9 * kQBlock;
+constexpr int kSlot = 8192;
+constexpr int kSlots = 10;
+constexpr int kOffRing = kQBytes;
+constexpr int kOffBar = kOffRing + kSlots * kSlot;
+constexpr int kSmem = 1024 + kOffBar + 512;
+static_assert(kSmem <= 232448, "shared memory per CTA");
+constexpr int kThreads = 256;
+constexpr uint32_t kTmemS = 256;                   // O in [0, 256), scores in 2 x 128 columns
+constexpr float kLn2 = 0.69314718055994530942f;
+// The running maximum moves, and O is rescaled, only when a tile exceeds it by 2^32: P stays below
+// 2^32, where bf16 has its full relative precision, and the sums stay far inside fp32.
+constexpr float kRescale = 32.0f;
+
+}  // namespace
+
+struct SharedParams {
+  const uint16_t* kv;
+  const int32_t* q_pos;
+  const int32_t* kv_len;
+  int64_t BT;
+  int T, P, S_max;
+  float scale_log2;
+  uint16_t* out;
+  float* lse;
+  int32_t* info;       // [pairs][2]: the item continued from the previous pair, the item cut at the end (-1: none)
+  float* part_ml;      // [pairs][2][256][2]: maximum (log2 units), sum
+  float* part_o;       // [pairs][2][64][256][4]: feature group, row, feature
+  int* status;
+};
+
+namespace {
+
+// Two tokens and their keys, in tiles: the prefix, then the own rows of token A's sequence (of both
+// tokens when they share it), then those of token B's.
+struct Unit {
+  int bA, bB, visA, visB;
+  int ptiles, tilesA, tiles;
+  bool same, hasB;
+};
+
+__device__ __forceinline__ int visible(const SharedParams& p, int64_t tok, int b) {
+  if (p.S_max == 0) return 0;
+  const int64_t v = (int64_t)__ldg(p.q_pos + tok) + 1;
+  const int64_t n = __ldg(p.kv_len + b);
+  return (int)max((int64_t)0, min(min(v, n), (int64_t)p.S_max));
+}
+
+__device__ __forceinline__ Unit load_unit(const SharedParams& p, int64_t u) {
+  Unit x;
+  const int64_t ta = 2 * u, tb = ta + 1;
+  x.hasB = tb < p.BT;
+  x.bA = (int)(ta / p.T);
+  x.bB = x.hasB ? (int)(tb / p.T) : x.bA;
+  x.same = x.bA == x.bB;
+  x.visA = visible(p, ta, x.bA);
+  x.visB = x.hasB ? visible(p, tb, x.bB) : 0;
+  x.ptiles = (p.P + kTile - 1) / kTile;
+  const int va = x.same ? max(x.visA, x.visB) : x.visA;
+  x.tilesA = (va + kTile - 1) / kTile;
+  const int tb_tiles = x.same ? 0 : (x.visB + kTile - 1) / kTile;
+  x.tiles = max(1, x.ptiles + x.tilesA + tb_tiles);   // a unit without keys still has its zeros to write
+  return x;
+}
+
+struct Tile {
+  int src;             // -1: the prefix, else the sequence
+  int k0;              // first key
+  int nA, nB;          // keys of the tile that token A / B sees
+  __device__ __forceinline__ int most() const { return max(nA, nB); }
+};
+
+__device__ __forceinline__ int clamp_tile(int v) { return max(0, min(kTile, v)); }
+
+__device__ __forceinline__ Tile get_tile(const SharedParams& p, const Unit& x, int t) {
+  Tile r;
+  if (t < x.ptiles) {
+    r.src = -1;
+    r.k0 = t * kTile;
+    r.nA = clamp_tile(p.P - r.k0);
+    r.nB = x.hasB ? r.nA : 0;
+  } else if (t - x.ptiles < x.tilesA) {
+    r.src = x.bA;
+    r.k0 = (t - x.ptiles) * kTile;
+    r.nA = clamp_tile(x.visA - r.k0);
+    r.nB = x.same ? clamp_tile(x.visB - r.k0) : 0;
+  } else {
+    r.src = x.bB;
+    r.k0 = (t - x.ptiles - x.tilesA) * kTile;
+    r.nA = 0;
+    r.nB = clamp_tile(x.visB - r.k0);
+  }
+  return r;
+}
+
+// The pieces of a pair's range of tiles, one item after the other; every role walks it for itself.
+struct Walk {
+  int64_t left;        // tiles left in the range
+  int64_t u;
+  int half, t0, t1;    // the piece: tiles [t0, t1) of (u, half)
+  Unit x;
+  __device__ __forceinline__ void start(const SharedParams& p, int64_t unit, int64_t off, int64_t count) {
+    left = count;
+    u = unit;
+    if (left <= 0) return;
+    x = load_unit(p, u);
+    half = off >= x.tiles;
+    t0 = (int)(off - (half ? x.tiles : 0));
+    t1 = (int)min((int64_t)x.tiles, t0 + left);
+  }
+  __device__ __forceinline__ bool valid() const { return left > 0; }
+  __device__ __forceinline__ void next(const SharedParams& p) {
+    left -= t1 - t0;
+    if (left <= 0) return;
+    if (half) {
+      ++u;
+      x = load_unit(p, u);
+    }
+    half ^= 1;
+    t0 = 0;
+    t1 = (int)min((int64_t)x.tiles, left);
+  }
+};
+
+// K rows of a tile that lie on this CTA: 64 keys, features [64 f, 64 f + 64)
+__device__ __forceinline__ void load_k(const CUtensorMap* pmap, const CUtensorMap* smap, const Tile& t, int f, uint32_t rank,
+                                       uint32_t dst, uint32_t bar) {
+  const int row = t.k0 + 64 * (int)rank;
+  if (t.src < 0) pair_load_2d(dst, pmap, bar, 64 * f, row);
+  else pair_load_3d(dst, smap, bar, 64 * f, row, t.src);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_shared_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap pk_map,
+                      const __grid_constant__ CUtensorMap pv_map, const __grid_constant__ CUtensorMap sk_map,
+                      const __grid_constant__ CUtensorMap sv_map, const SharedParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // both CTAs of a pair see the same offsets: the MMA reads them with one descriptor
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* full = bars;                 // leader: both CTAs' parts of the slot have landed
+  uint64_t* empty = full + kSlots;       // both: the MMAs that read the slot are done
+  uint64_t* s_full = empty + kSlots;     // both [2]: scores ready
+  uint64_t* p_full = s_full + 2;         // leader [2]: probabilities of both CTAs written
+  uint64_t* pv_done = p_full + 2;        // both [2]: P V of the tile done
+  uint64_t* q_full = pv_done + 2;        // leader: Q of both CTAs landed
+  uint64_t* q_empty = q_full + 1;        // both: the piece's Q K^T done
+  uint64_t* o_free = q_empty + 1;        // leader: both CTAs have read O
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+  __shared__ long long scan_sh[kThreads / 32];
+  __shared__ long long start_sh[2];      // first unit of this pair's range, offset in its 2 x tiles
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = pair_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], 2);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 8);
+      mbar_init(&pv_done[i], 1);
+    }
+    mbar_init(q_full, 2);
+    mbar_init(q_empty, 1);
+    mbar_init(o_free, 8);
+    fence_barrier_init();
+  }
+  if (warp == 2) pair_tmem_alloc(&tmem_base_sh, 512);
+  grid_dep_wait();                       // lengths, queries and caches may come from the preceding kernel
+  grid_dep_launch();
+
+  // The pair's range of tiles: thread i sums the units [i * per, (i + 1) * per).
+  const int64_t units = (p.BT + 1) / 2;
+  const int64_t per = (units + kThreads - 1) / kThreads;
+  const int64_t ua = min(units, tid * per), ub = min(units, ua + per);
+  long long sum = 0;
+  for (int64_t u = ua; u < ub; ++u) sum += 2 * load_unit(p, u).tiles;
+  long long pre = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, pre, d);
+    if (lane >= d) pre += o;
+  }
+  if (lane == 31) scan_sh[warp] = pre;
+  if (tid == 0) start_sh[0] = start_sh[1] = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0, base = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) base = total;
+    total += scan_sh[w];
+  }
+  const long long excl = base + pre - sum;
+  // no more pairs than tiles: the join walks over consecutive pairs, none of them without a tile
+  const long long active = min((long long)pairs, total);
+  const long long lo = pair < active ? total * pair / active : total;
+  const long long hi = pair < active ? total * (pair + 1) / active : total;
+  if (sum > 0 && lo >= excl && lo < excl + sum) {
+    long long off = lo - excl;
+    int64_t u = ua;
+    for (; u < ub; ++u) {
+      const long long n = 2 * load_unit(p, u).tiles;
+      if (off < n) break;
+      off -= n;
+    }
+    start_sh[0] = u;
+    start_sh[1] = off;
+  }
+  __syncthreads();
+  pair_barrier();                        // barriers of both CTAs are initialised, both hold their TMEM
+  const uint32_t tmem = tmem_base_sh;
+  Walk w;
+  w.start(p, start_sh[0], start_sh[1], hi - lo);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ loads
+    const bool el = elect_one();
+    const uint32_t ring = smem_u32(smem + kOffRing);
+    int slot = 0, round = 0;
+    bool ok = true;
+    auto acquire = [&]() {
+      if (round > 0 && !mbar_wait_cluster(&empty[slot], (round + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY))
+        ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+    };
+    auto advance = [&]() {
+      if (++slot == kSlots) {
+        slot = 0;
+        ++round;
+      }
+    };
+    auto k_tile = [&](const Tile& t) {
+      for (int f = 0; ok && f < 9; ++f) {
+        acquire();
+        if (!ok) break;
+        if (el) {
+          const uint32_t bar = leader_addr(&full[slot]);
+          arrive_expect_tx_cluster(bar, kSlot);
+          load_k(&pk_map, &sk_map, t, f, rank, ring + slot * kSlot, bar);
+        }
+        advance();
+      }
+    };
+    auto v_tile = [&](const Tile& t, int half) {
+      const int n = t.most();
+      const int feat = 256 * half + 128 * (int)rank;
+      for (int kb = 0; ok && kb < n; kb += 32) {
+        acquire();
+        if (!ok) break;
+        const uint32_t dst = ring + slot * kSlot, bar = leader_addr(&full[slot]);
+        if (t.src < 0 || n - kb >= 32) {
+          if (el) {
+            arrive_expect_tx_cluster(bar, kSlot);
+            for (int i = 0; i < 2; ++i) {
+              if (t.src < 0) pair_load_2d(dst + 4096 * i, &pv_map, bar, feat + 64 * i, t.k0 + kb);
+              else pair_load_3d(dst + 4096 * i, &sv_map, bar, feat + 64 * i, t.k0 + kb, t.src);
+            }
+          }
+        } else {
+          // the rows behind the last visible key may hold anything, and 0 * NaN is NaN: the warp
+          // copies the visible rows itself and puts zeros behind them
+          const uint16_t* src = p.kv + ((int64_t)t.src * p.S_max + t.k0 + kb) * kDqk + feat;
+          uint4 v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4), c = lane & 15;      // row, 16-byte chunk of its 256 bytes
+            v[i] = r < n - kb ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * kDqk) + c) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r = 2 * i + (lane >> 4), c = lane & 15;
+            const uint32_t a = dst + 4096 * (c >> 3) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z),
+                         "r"(v[i].w)
+                         : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (el) arrive_cluster(bar);
+        }
+        advance();
+      }
+    };
+    int piece = 0;
+    for (; ok && w.valid(); w.next(p)) {
+      if (get_tile(p, w.x, w.t0).most() == 0) continue;          // a unit without keys
+      if (piece > 0) {
+        if (!mbar_wait_cluster(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+      }
+      if (el) {
+        const uint32_t bar = leader_addr(q_full);
+        arrive_expect_tx_cluster(bar, kQBytes);
+        for (int f = 0; f < 9; ++f)
+          pair_load_2d(smem_u32(smem) + f * kQBlock, &q_map, bar, 64 * f, (int32_t)((2 * w.u + rank) * kHeads));
+      }
+      ++piece;
+      Tile prev = get_tile(p, w.x, w.t0);
+      k_tile(prev);
+      for (int t = w.t0 + 1; ok && t < w.t1; ++t) {
+        const Tile cur = get_tile(p, w.x, t);
+        k_tile(cur);
+        v_tile(prev, w.half);
+        prev = cur;
+      }
+      if (ok) v_tile(prev, w.half);
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------------------------ MMA issue (leader)
+    const bool el = elect_one();
+    const uint32_t idesc_s = idesc_f32acc(1, 1, 256, kTile, 0, 0);
+    const uint32_t idesc_o = idesc_f32acc(1, 1, 256, 256, 0, 1);
+    const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem));
+    const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffRing));
+    const uint64_t v_desc = sdesc_mnmajor_sw128(smem_u32(smem + kOffRing), 4096, 1024);
+    int slot = 0, round = 0, piece = 0;
+    uint32_t g = 0;                       // tiles so far
+    bool ok = true;
+    auto wait_full = [&]() {
+      if (!mbar_wait_cluster(&full[slot], round & 1, &abort_flag, p.status, DSA_SITE_SHARED_FULL)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+    };
+    auto advance = [&]() {
+      if (++slot == kSlots) {
+        slot = 0;
+        ++round;
+      }
+    };
+    auto qk = [&](uint32_t buf) {
+      const uint32_t d = tmem + kTmemS + buf * kTile;
+      for (int f = 0; ok && f < 9; ++f) {
+        wait_full();
+        if (!ok) break;
+        if (el) {
+          const uint64_t a = q_desc + (uint64_t)((f * kQBlock) >> 4), b = k_desc + (uint64_t)((slot * kSlot) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pair_mma_ss(d, a + 2 * k, b + 2 * k, idesc_s, (f | k) != 0);
+          pair_commit(&empty[slot]);
+        }
+        advance();
+      }
+      if (ok && el) pair_commit(&s_full[buf]);
+    };
+    for (; ok && w.valid(); w.next(p)) {
+      Tile cur = get_tile(p, w.x, w.t0);
+      if (cur.most() == 0) continue;
+      if (!mbar_wait_cluster(q_full, piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q)) ok = false;
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      bool startedA = false, startedB = false;
+      qk(g & 1);
+      for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+        if (t + 1 < w.t1) qk((g + 1) & 1);
+        else if (el) pair_commit(q_empty);
+        if (!ok) break;
+        if (t == w.t0 && piece > 0 &&
+            !mbar_wait_cluster(o_free, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O))
+          ok = false;
+        if (!mbar_wait_cluster(&p_full[g & 1], (g >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        cur = get_tile(p, w.x, t);
+        // the token that sees nothing of the tile keeps its O
+        const uint32_t off0 = cur.nA > 0 ? 0u : 0xffffffffu, off1 = cur.nB > 0 ? 0u : 0xffffffffu;
+        bool acc = (cur.nA > 0 && startedA) || (cur.nB > 0 && startedB);
+        startedA |= cur.nA > 0;
+        startedB |= cur.nB > 0;
+        const int n = cur.most();
+        const uint32_t a = tmem + kTmemS + (g & 1) * kTile;
+        for (int kb = 0; ok && kb < n; kb += 32) {
+          wait_full();
+          if (!ok) break;
+          if (el) {
+            const uint64_t b = v_desc + (uint64_t)((slot * kSlot) >> 4);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if ((off0 | off1) == 0) pair_mma_ts(tmem, a + kb / 2 + 8 * k, b + 128 * k, idesc_o, acc || k > 0);
+              else pair_mma_ts_masked(tmem, a + kb / 2 + 8 * k, b + 128 * k, idesc_o, off0, off1, acc || k > 0);
+            }
+            pair_commit(&empty[slot]);
+          }
+          acc = true;
+          advance();
+        }
+        if (ok && el) pair_commit(&pv_done[g & 1]);
+      }
+      ++piece;
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax, one thread per row
+    const int row = tid - 128;            // head; TMEM lane
+    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t g = 0;
+    bool ok = true;
+    int32_t info_cont = -1, info_head = -1;
+    for (; ok && w.valid(); w.next(p)) {
+      const int64_t tok = 2 * w.u + rank;
+      float m = -INFINITY, l = 0.f;
+      bool any = false;
+      for (int t = w.t0; ok && t < w.t1; ++t) {
+        const Tile tile = get_tile(p, w.x, t);
+        if (tile.most() == 0) continue;
+        const int n = rank == 0 ? tile.nA : tile.nB;
+        const uint32_t buf = g & 1, ph = (g >> 1) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s_full[buf], ph, &abort_flag, p.status, DSA_SITE_SHARED_S))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (n > 0) {
+          uint32_t r[4][32];
+          const uint32_t s = t_row + kTmemS + buf * kTile;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s + 32 * c, r[c]);
+          tmem_ld_wait();
+          if (n < kTile) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i >= n) r[c][i] = 0xff800000u;
+          }
+          float mx4[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            mx4[c] = __uint_as_float(r[c][0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i) mx4[c] = fmaxf(mx4[c], __uint_as_float(r[c][i]));
+          }
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+          float alpha = 1.f;
+          bool rescale = false;
+          if (mx > m + kRescale) {
+            alpha = exp2_approx(m - mx);  // 0 for the first
+            rescale = m != -INFINITY;
+            m = mx;
+          }
+          const float mm = m == -INFINITY ? 0.f : m;   // every score -inf: e^-inf = 0, not NaN
+          float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t pk[2][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float e0 = exp2_approx(fmaf(__uint_as_float(r[c][i]), p.scale_log2, -mm));
+              const float e1 = exp2_approx(fmaf(__uint_as_float(r[c][i + 1]), p.scale_log2, -mm));
+              sum4[(i >> 1) & 3] += e0 + e1;
+              pk[c >> 1][(c & 1) * 16 + i / 2] = pack_bf16(e0, e1);
+            }
+          }
+          l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+          if (__any_sync(0xffffffffu, rescale)) {
+            // P V of every earlier tile has to be in O first
+            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag,
+                                                           p.status, DSA_SITE_SHARED_O))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[32];
+              tmem_ld32(t_row + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (rescale ? alpha : 1.f));
+              tmem_st32(t_row + 32 * c, o);
+            }
+          }
+          any = true;
+          tmem_st32(s, pk[0]);
+          tmem_st32(s + 32, pk[1]);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(leader_addr(&p_full[buf]));
+        ++g;
+      }
+      if (!ok) break;
+      // ---- the piece is done: output, or a partial for the join
+      const bool whole = w.t0 == 0 && w.t1 == w.x.tiles;
+      const int where = w.t0 == 0 ? 1 : 0;
+      if (!whole) (where ? info_head : info_cont) = (int32_t)(2 * w.u + w.half);
+      const bool had = get_tile(p, w.x, w.t0).most() > 0;
+      if (had) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status,
+                                                       DSA_SITE_SHARED_O))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      const int64_t slot = (int64_t)pair * 2 + where;
+      const int prow = (int)rank * kHeads + row;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      if (whole) {
+        if (tok < p.BT && w.half == 0 && p.lse)
+          p.lse[tok * kHeads + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        *reinterpret_cast<float2*>(p.part_ml + (slot * 256 + prow) * 2) = make_float2(m, l);
+      }
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        uint32_t o[32];
+        if (any) {
+          tmem_ld32(t_row + 32 * c, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (whole) {
+          if (tok < p.BT) {
+            uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * kHeads + row) * kDv + 256 * w.half + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 v;
+              v.x = pack_bf16(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
+              v.y = pack_bf16(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
+              v.z = pack_bf16(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
+              v.w = pack_bf16(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
+              dst[i] = v;
+            }
+          }
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (slot * 64 + 8 * c) * 256 + prow;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i * 256] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      if (had) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(leader_addr(o_free));
+      }
+    }
+    if (rank == 0 && tid == 128) {
+      p.info[2 * pair] = info_cont;
+      p.info[2 * pair + 1] = info_head;
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  pair_barrier();                        // nothing of the pair is still in flight towards either CTA
+  if (warp == 2) pair_tmem_dealloc(tmem, 512);
+}
+
+// Joins the pieces of items that were cut: block (p, y) takes 32 rows of the item whose first piece
+// is the last one of pair p; the pieces that follow are the first ones of the next pairs.
+__global__ void __launch_bounds__(256) mla_shared_join_kernel(const SharedParams p, int pairs) {
+  const int pair = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int item = p.info[2 * pair + 1];
+  if (item < 0) return;
+  const int row = blockIdx.y * 32 + lane;
+  const int64_t tok = 2 * (int64_t)(item >> 1) + (row >> 7);
+  const int head = row & 127, half = item & 1;
+  if (tok >= p.BT) return;
+  int end = pair + 1;
+  while (end < pairs && p.info[2 * end] == item) ++end;
+  auto slot_of = [&](int q) { return q == pair ? (int64_t)pair * 2 + 1 : (int64_t)q * 2; };
+  float m = -INFINITY;
+  for (int q = pair; q < end; ++q) m = fmaxf(m, p.part_ml[(slot_of(q) * 256 + row) * 2]);
+  float l = 0.f;
+  float4 acc[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = pair; q < end; ++q) {
+    const int64_t slot = slot_of(q);
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * 256 + row) * 2);
+    // a piece without a visible key has sum 0 and no maximum
+    const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - m);
+    l += ml.y * f;
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * 64 + warp * 8) * 256 + row;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = src[i * 256];
+      acc[i].x = fmaf(v.x, f, acc[i].x);
+      acc[i].y = fmaf(v.y, f, acc[i].y);
+      acc[i].z = fmaf(v.z, f, acc[i].z);
+      acc[i].w = fmaf(v.w, f, acc[i].w);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * kHeads + head) * kDv + 256 * half + 32 * warp);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 a = acc[2 * i], b = acc[2 * i + 1];
+    dst[i] = make_uint4(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv), pack_bf16(b.x * inv, b.y * inv),
+                        pack_bf16(b.z * inv, b.w * inv));
+  }
+  if (warp == 0 && half == 0 && p.lse) p.lse[tok * kHeads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+namespace {
+
+// Pairs of the launch: one per two SMs, at most one per tile.
+int shared_pairs(int64_t BT, int T, int P, int S_max) {
+  const int64_t units = (BT + 1) / 2;
+  const int64_t own = (S_max + kTile - 1) / kTile;
+  const int64_t tiles = std::max<int64_t>(1, (P + kTile - 1) / kTile + 2 * own);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(dsa_host::device_sm_count() / 2, 2 * units * tiles));
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+size_t mla_shared_workspace_size(int B, int T, int P, int S_max) {
+  const size_t pairs = (size_t)shared_pairs((int64_t)B * T, T, P, S_max);
+  return align256(pairs * 8) + pairs * 2 * 256 * 8 + pairs * 2 * 64 * 256 * 16;
+}
+
+int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const uint16_t* kv, const int32_t* q_pos,
+                      const int32_t* kv_len, int B, int T, int S_max, float softmax_scale, uint16_t* out, float* lse,
+                      void* workspace, size_t ws_bytes, cudaStream_t stream, int* status) {
+  if (!workspace || ws_bytes < mla_shared_workspace_size(B, T, P, S_max)) return DSA_ERR_WORKSPACE;
+  SharedParams p;
+  p.kv = kv;
+  p.q_pos = q_pos;
+  p.kv_len = kv_len;
+  p.BT = (int64_t)B * T;
+  p.T = T;
+  p.P = P;
+  p.S_max = S_max;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = out;
+  p.lse = lse;
+  p.status = status;
+  const int pairs = shared_pairs(p.BT, T, P, S_max);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.info = reinterpret_cast<int32_t*>(ws);
+  ws += align256((size_t)pairs * 8);
+  p.part_ml = reinterpret_cast<float*>(ws);
+  ws += (size_t)pairs * 2 * 256 * 8;
+  p.part_o = reinterpret_cast<float*>(ws);
+
+  const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const uint64_t row = kDqk * 2;
+  CUtensorMap q_map, pk, pv, sk, sv;
+  if (!dsa_host::encode_tensor_map_2d(&q_map, dt, const_cast<uint16_t*>(q), kDqk, (uint64_t)p.BT * kHeads, row, 64, kHeads,
+                                      sw))
+    return DSA_ERR_CUDA;
+  pk = pv = sk = sv = q_map;                         // an empty source is never loaded from
+  if (P > 0 &&
+      (!dsa_host::encode_tensor_map_2d(&pk, dt, const_cast<uint16_t*>(prefix), kDqk, (uint64_t)P, row, 64, 64, sw) ||
+       !dsa_host::encode_tensor_map_2d(&pv, dt, const_cast<uint16_t*>(prefix), kDqk, (uint64_t)P, row, 64, 32, sw)))
+    return DSA_ERR_CUDA;
+  if (S_max > 0) {
+    const uint64_t dims[3] = {(uint64_t)kDqk, (uint64_t)S_max, (uint64_t)B};
+    const uint64_t strides[2] = {row, row * (uint64_t)S_max};
+    const uint32_t kbox[3] = {64, 64, 1}, vbox[3] = {64, 32, 1};
+    if (!dsa_host::encode_tensor_map_3d(&sk, dt, const_cast<uint16_t*>(kv), dims, strides, kbox, sw) ||
+        !dsa_host::encode_tensor_map_3d(&sv, dt, const_cast<uint16_t*>(kv), dims, strides, vbox, sw))
+      return DSA_ERR_CUDA;
+  }
+  static uint64_t seen[dsa_host::kMaxSetupDevices];
+  if (dsa_host::needs_setup(seen, nullptr)) {
+    if (cudaFuncSetAttribute(mla_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    dsa_host::mark_setup(seen);
+  }
+  int rc = dsa_host::launch_pairs(mla_shared_kernel, (unsigned)pairs, kThreads, kSmem, stream, q_map, pk, pv, sk, sv, p);
+  if (rc != DSA_OK) return rc;
+  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)pairs, 8), dim3(256), 0, stream, p, pairs);
+}
+
+}  // namespace dsa
