@@ -15,9 +15,9 @@
 // a second kernel joins. Every pair holds at most two such pieces, so the workspace is bounded
 // whatever the lengths are, and the device alone reads the lengths.
 //
-// Per CTA: Q (128 x 576, 144 KB) stays in shared memory; K and V stream through one ring of 8 KB
-// blocks in the order the MMAs consume them (K: 64 keys x 64 features, this CTA's half of the
-// tile's keys; V: 32 keys x 128 features, its half of the 256 output features). TMEM: O [0, 256),
+// Per CTA: Q (128 x 576, 144 KB) stays in shared memory; K and V stream through one ring of 16 KB
+// slots of 64 keys x 128 features in the order the MMAs consume them (K: this CTA's half of the
+// tile's keys, five slots; V: its half of the 256 output features, two slots). TMEM: O [0, 256),
 // two score buffers of 128 columns; the probabilities (bf16) replace the scores they came from and
 // are the A operand of P V. Q K^T of tile j + 1 runs while the softmax of tile j does.
 #include <math.h>
@@ -36,8 +36,8 @@ constexpr int kDqk = 576, kDv = 512;
 constexpr int kTile = 128;                         // keys per tile
 constexpr int kQBlock = kHeads * 128;              // 16 KB: 64 features of 128 rows
 constexpr int kQBytes = 9 * kQBlock;
-constexpr int kSlot = 8192;
-constexpr int kSlots = 10;
+constexpr int kSlot = 16384;                       // 64 keys x two blocks of 64 features
+constexpr int kSlots = 5;
 constexpr int kOffRing = kQBytes;
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
 constexpr int kSmem = 1024 + kOffBar + 512;
@@ -159,20 +159,18 @@ struct Walk {
   }
 };
 
-// K rows of a tile that lie on this CTA: 64 keys, features [64 f, 64 f + 64)
-__device__ __forceinline__ void load_k(const CUtensorMap* pmap, const CUtensorMap* smap, const Tile& t, int f, uint32_t rank,
-                                       uint32_t dst, uint32_t bar) {
-  const int row = t.k0 + 64 * (int)rank;
-  if (t.src < 0) pair_load_2d(dst, pmap, bar, 64 * f, row);
-  else pair_load_3d(dst, smap, bar, 64 * f, row, t.src);
+// Rows [row, row + 64) of a tile's source, feature blocks [block, block + 2) of 64: [block][row][64]
+__device__ __forceinline__ void load_slot(const CUtensorMap* pmap, const CUtensorMap* smap, int src, int row, int block,
+                                          uint32_t dst, uint32_t bar) {
+  if (src < 0) pair_load_3d(dst, pmap, bar, 0, row, block);
+  else pair_load_4d(dst, smap, bar, 0, row, block, src);
 }
 
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1)
-    mla_shared_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap pk_map,
-                      const __grid_constant__ CUtensorMap pv_map, const __grid_constant__ CUtensorMap sk_map,
-                      const __grid_constant__ CUtensorMap sv_map, const SharedParams p) {
+    mla_shared_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap p_map,
+                      const __grid_constant__ CUtensorMap s_map, const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // both CTAs of a pair see the same offsets: the MMA reads them with one descriptor
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -259,14 +257,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk w;
   w.start(p, start_sh[0], start_sh[1], hi - lo);
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------------ loads
+    // Waiting for a slot and issuing its load take one warp about 400 cycles, more than the MMAs of a
+    // block (260): three warps take the blocks in turn (shared_chunk 3059 -> 0 us).
+    const int mine = warp == 0 ? 0 : warp - 1;
+    int turn = 0;
     const bool el = elect_one();
     const uint32_t ring = smem_u32(smem + kOffRing);
     int slot = 0, round = 0;
     bool ok = true;
     auto acquire = [&]() {
-      if (round > 0 && !mbar_wait_cluster(&empty[slot], (round + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY))
+      if (round > 0 && !mbar_wait(&empty[slot], (round + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY))
         ok = false;
       ok = __all_sync(0xffffffffu, ok);
     };
@@ -275,68 +277,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         slot = 0;
         ++round;
       }
+      if (++turn == 3) turn = 0;
     };
     auto k_tile = [&](const Tile& t) {
-      for (int f = 0; ok && f < 9; ++f) {
+      for (int f = 0; ok && f < 9; f += 2, advance()) {
+        if (turn != mine) continue;
         acquire();
         if (!ok) break;
         if (el) {
           const uint32_t bar = leader_addr(&full[slot]);
-          arrive_expect_tx_cluster(bar, kSlot);
-          load_k(&pk_map, &sk_map, t, f, rank, ring + slot * kSlot, bar);
+          arrive_expect_tx_cluster(bar, kSlot);          // there is no block 9: zeros
+          load_slot(&p_map, &s_map, t.src, t.k0 + 64 * (int)rank, f, ring + slot * kSlot, bar);
         }
-        advance();
       }
     };
     auto v_tile = [&](const Tile& t, int half) {
       const int n = t.most();
-      const int feat = 256 * half + 128 * (int)rank;
-      for (int kb = 0; ok && kb < n; kb += 32) {
+      for (int kb = 0; ok && kb < n; kb += 64, advance()) {
+        if (turn != mine) continue;
         acquire();
         if (!ok) break;
         const uint32_t dst = ring + slot * kSlot, bar = leader_addr(&full[slot]);
-        if (t.src < 0 || n - kb >= 32) {
+        const int block = 4 * half + 2 * (int)rank;
+        if (t.src < 0 || n - kb >= 64) {
           if (el) {
             arrive_expect_tx_cluster(bar, kSlot);
-            for (int i = 0; i < 2; ++i) {
-              if (t.src < 0) pair_load_2d(dst + 4096 * i, &pv_map, bar, feat + 64 * i, t.k0 + kb);
-              else pair_load_3d(dst + 4096 * i, &sv_map, bar, feat + 64 * i, t.k0 + kb, t.src);
-            }
+            load_slot(&p_map, &s_map, t.src, t.k0 + kb, block, dst, bar);
           }
         } else {
           // the rows behind the last visible key may hold anything, and 0 * NaN is NaN: the warp
           // copies the visible rows itself and puts zeros behind them
-          const uint16_t* src = p.kv + ((int64_t)t.src * p.S_max + t.k0 + kb) * kDqk + feat;
-          uint4 v[16];
+          const uint16_t* src = p.kv + ((int64_t)t.src * p.S_max + t.k0 + kb) * kDqk + 64 * block;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint4 v[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4), c = lane & 15;      // row, 16-byte chunk of its 256 bytes
-            v[i] = r < n - kb ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * kDqk) + c) : make_uint4(0, 0, 0, 0);
-          }
+            for (int i = 0; i < 16; ++i) {
+              const int r = 32 * h + 2 * i + (lane >> 4), c = lane & 15;    // row, 16-byte chunk of its 256 bytes
+              v[i] = r < n - kb ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * kDqk) + c) : make_uint4(0, 0, 0, 0);
+            }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int r = 2 * i + (lane >> 4), c = lane & 15;
-            const uint32_t a = dst + 4096 * (c >> 3) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z),
-                         "r"(v[i].w)
-                         : "memory");
+            for (int i = 0; i < 16; ++i) {
+              const int r = 32 * h + 2 * i + (lane >> 4), c = lane & 15;
+              const uint32_t a = dst + 8192 * (c >> 3) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z),
+                           "r"(v[i].w)
+                           : "memory");
+            }
           }
           fence_proxy_async_smem();
+          cluster_fence();
           __syncwarp();
           if (el) arrive_cluster(bar);
         }
-        advance();
       }
     };
     int piece = 0;
     for (; ok && w.valid(); w.next(p)) {
       if (get_tile(p, w.x, w.t0).most() == 0) continue;          // a unit without keys
-      if (piece > 0) {
-        if (!mbar_wait_cluster(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY)) ok = false;
+      if (mine == 0 && piece > 0) {
+        if (!mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
-      if (el) {
+      if (mine == 0 && el) {
         const uint32_t bar = leader_addr(q_full);
         arrive_expect_tx_cluster(bar, kQBytes);
         for (int f = 0; f < 9; ++f)
@@ -353,89 +357,88 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) v_tile(prev, w.half);
     }
-  } else if (warp == 1 && rank == 0) {
-    // ------------------------------------------------------------------ MMA issue (leader)
-    const bool el = elect_one();
-    const uint32_t idesc_s = idesc_f32acc(1, 1, 256, kTile, 0, 0);
-    const uint32_t idesc_o = idesc_f32acc(1, 1, 256, 256, 0, 1);
-    const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem));
-    const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffRing));
-    const uint64_t v_desc = sdesc_mnmajor_sw128(smem_u32(smem + kOffRing), 4096, 1024);
-    int slot = 0, round = 0, piece = 0;
-    uint32_t g = 0;                       // tiles so far
-    bool ok = true;
-    auto wait_full = [&]() {
-      if (!mbar_wait_cluster(&full[slot], round & 1, &abort_flag, p.status, DSA_SITE_SHARED_FULL)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      tc_fence_after();
-    };
-    auto advance = [&]() {
-      if (++slot == kSlots) {
-        slot = 0;
-        ++round;
-      }
-    };
-    auto qk = [&](uint32_t buf) {
-      const uint32_t d = tmem + kTmemS + buf * kTile;
-      for (int f = 0; ok && f < 9; ++f) {
-        wait_full();
-        if (!ok) break;
-        if (el) {
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issue: one thread of the leader
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc_s = idesc_f32acc(1, 1, 256, kTile, 0, 0);
+      const uint32_t idesc_o = idesc_f32acc(1, 1, 256, 256, 0, 1);
+      const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem));
+      const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffRing));
+      const uint64_t v_desc = sdesc_mnmajor_sw128(smem_u32(smem + kOffRing), 8192, 1024);
+      int slot = 0, piece = 0;
+      uint32_t ph = 0, g = 0;             // ring phase, tiles so far
+      bool ok = true;
+      auto wait_full = [&]() {
+        if (!mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_SHARED_FULL)) ok = false;
+        tc_fence_after();
+      };
+      auto advance = [&]() {
+        if (++slot == kSlots) {
+          slot = 0;
+          ph ^= 1;
+        }
+      };
+      auto qk = [&](uint32_t buf) {
+        const uint32_t d = tmem + kTmemS + buf * kTile;
+#pragma unroll
+        for (int f = 0; f < 9; f += 2) {
+          if (ok) wait_full();
+          if (!ok) break;
           const uint64_t a = q_desc + (uint64_t)((f * kQBlock) >> 4), b = k_desc + (uint64_t)((slot * kSlot) >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) pair_mma_ss(d, a + 2 * k, b + 2 * k, idesc_s, (f | k) != 0);
+          for (int k = 0; k < 8; ++k)
+            if (f + (k >> 2) < 9)
+              pair_mma_ss(d, a + 2 * (k & 3) + (k >> 2) * (kQBlock >> 4), b + 2 * (k & 3) + (k >> 2) * (8192 >> 4), idesc_s,
+                          (f | k) != 0);
           pair_commit(&empty[slot]);
-        }
-        advance();
-      }
-      if (ok && el) pair_commit(&s_full[buf]);
-    };
-    for (; ok && w.valid(); w.next(p)) {
-      Tile cur = get_tile(p, w.x, w.t0);
-      if (cur.most() == 0) continue;
-      if (!mbar_wait_cluster(q_full, piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q)) ok = false;
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      bool startedA = false, startedB = false;
-      qk(g & 1);
-      for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-        if (t + 1 < w.t1) qk((g + 1) & 1);
-        else if (el) pair_commit(q_empty);
-        if (!ok) break;
-        if (t == w.t0 && piece > 0 &&
-            !mbar_wait_cluster(o_free, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O))
-          ok = false;
-        if (!mbar_wait_cluster(&p_full[g & 1], (g >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        cur = get_tile(p, w.x, t);
-        // the token that sees nothing of the tile keeps its O
-        const uint32_t off0 = cur.nA > 0 ? 0u : 0xffffffffu, off1 = cur.nB > 0 ? 0u : 0xffffffffu;
-        bool acc = (cur.nA > 0 && startedA) || (cur.nB > 0 && startedB);
-        startedA |= cur.nA > 0;
-        startedB |= cur.nB > 0;
-        const int n = cur.most();
-        const uint32_t a = tmem + kTmemS + (g & 1) * kTile;
-        for (int kb = 0; ok && kb < n; kb += 32) {
-          wait_full();
-          if (!ok) break;
-          if (el) {
-            const uint64_t b = v_desc + (uint64_t)((slot * kSlot) >> 4);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              if ((off0 | off1) == 0) pair_mma_ts(tmem, a + kb / 2 + 8 * k, b + 128 * k, idesc_o, acc || k > 0);
-              else pair_mma_ts_masked(tmem, a + kb / 2 + 8 * k, b + 128 * k, idesc_o, off0, off1, acc || k > 0);
-            }
-            pair_commit(&empty[slot]);
-          }
-          acc = true;
           advance();
         }
-        if (ok && el) pair_commit(&pv_done[g & 1]);
+        if (ok) pair_commit(&s_full[buf]);
+      };
+      for (; ok && w.valid(); w.next(p)) {
+        Tile cur = get_tile(p, w.x, w.t0);
+        if (cur.most() == 0) continue;
+        if (!mbar_wait(q_full, piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q)) break;
+        tc_fence_after();
+        bool startedA = false, startedB = false;
+        qk(g & 1);
+        for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+          if (t + 1 < w.t1) qk((g + 1) & 1);
+          else pair_commit(q_empty);
+          if (!ok) break;
+          cur = get_tile(p, w.x, t);
+          // the token that sees nothing of the tile keeps its O
+          const uint32_t off0 = cur.nA > 0 ? 0u : 0xffffffffu, off1 = cur.nB > 0 ? 0u : 0xffffffffu;
+          bool acc = (cur.nA > 0 && startedA) || (cur.nB > 0 && startedB);
+          startedA |= cur.nA > 0;
+          startedB |= cur.nB > 0;
+          const int n = cur.most();
+          const uint32_t a = tmem + kTmemS + (g & 1) * kTile;
+          if (t == w.t0 && piece > 0 && !mbar_wait(o_free, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O))
+            ok = false;
+          if (!ok || !mbar_wait(&p_full[g & 1], (g >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) ok = false;
+          tc_fence_after();
+          for (int kb = 0; ok && kb < n; kb += 64) {
+            wait_full();
+            if (!ok) break;
+            const bool part = n - kb < 64;
+            if (cur.src >= 0 && part) cluster_fence();               // both CTAs' warps wrote this slot
+            const uint64_t b = v_desc + (uint64_t)((slot * kSlot) >> 4);
+            if ((off0 | off1) == 0 && !part) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) pair_mma_ts(tmem, a + kb / 2 + 8 * k, b + 128 * k, idesc_o, acc || k > 0);
+            } else {
+              for (int k = 0; k < 4 && kb + 16 * k < n; ++k)
+                pair_mma_ts_masked(tmem, a + kb / 2 + 8 * k, b + 128 * k, idesc_o, off0, off1, acc || k > 0);
+            }
+            pair_commit(&empty[slot]);
+            acc = true;
+            advance();
+          }
+          if (ok) pair_commit(&pv_done[g & 1]);
+        }
+        ++piece;
       }
-      ++piece;
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ softmax, one thread per row
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (tile.most() == 0) continue;
         const int n = rank == 0 ? tile.nA : tile.nB;
         const uint32_t buf = g & 1, ph = (g >> 1) & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&s_full[buf], ph, &abort_flag, p.status, DSA_SITE_SHARED_S))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], ph, &abort_flag, p.status, DSA_SITE_SHARED_S))) {
           ok = false;
           break;
         }
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
           if (__any_sync(0xffffffffu, rescale)) {
             // P V of every earlier tile has to be in O first
-            if (!__all_sync(0xffffffffu, mbar_wait_cluster(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag,
+            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag,
                                                            p.status, DSA_SITE_SHARED_O))) {
               ok = false;
               break;
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!whole) (where ? info_head : info_cont) = (int32_t)(2 * w.u + w.half);
       const bool had = get_tile(p, w.x, w.t0).most() > 0;
       if (had) {
-        if (!__all_sync(0xffffffffu, mbar_wait_cluster(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status,
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status,
                                                        DSA_SITE_SHARED_O))) {
           ok = false;
           break;
@@ -692,22 +695,20 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
   const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   const uint64_t row = kDqk * 2;
-  CUtensorMap q_map, pk, pv, sk, sv;
+  CUtensorMap q_map, pm, sm;
   if (!dsa_host::encode_tensor_map_2d(&q_map, dt, const_cast<uint16_t*>(q), kDqk, (uint64_t)p.BT * kHeads, row, 64, kHeads,
                                       sw))
     return DSA_ERR_CUDA;
-  pk = pv = sk = sv = q_map;                         // an empty source is never loaded from
-  if (P > 0 &&
-      (!dsa_host::encode_tensor_map_2d(&pk, dt, const_cast<uint16_t*>(prefix), kDqk, (uint64_t)P, row, 64, 64, sw) ||
-       !dsa_host::encode_tensor_map_2d(&pv, dt, const_cast<uint16_t*>(prefix), kDqk, (uint64_t)P, row, 64, 32, sw)))
-    return DSA_ERR_CUDA;
+  pm = sm = q_map;                                   // an empty source is never loaded from
+  // feature, row, block of 64 features (, sequence): one box is two blocks of 64 rows, block by block
+  const uint32_t box[4] = {64, 64, 2, 1};
+  if (P > 0) {
+    const uint64_t dims[3] = {64, (uint64_t)P, 9}, strides[2] = {row, 128};
+    if (!dsa_host::encode_tensor_map(&pm, dt, 3, const_cast<uint16_t*>(prefix), dims, strides, box, sw)) return DSA_ERR_CUDA;
+  }
   if (S_max > 0) {
-    const uint64_t dims[3] = {(uint64_t)kDqk, (uint64_t)S_max, (uint64_t)B};
-    const uint64_t strides[2] = {row, row * (uint64_t)S_max};
-    const uint32_t kbox[3] = {64, 64, 1}, vbox[3] = {64, 32, 1};
-    if (!dsa_host::encode_tensor_map_3d(&sk, dt, const_cast<uint16_t*>(kv), dims, strides, kbox, sw) ||
-        !dsa_host::encode_tensor_map_3d(&sv, dt, const_cast<uint16_t*>(kv), dims, strides, vbox, sw))
-      return DSA_ERR_CUDA;
+    const uint64_t dims[4] = {64, (uint64_t)S_max, 9, (uint64_t)B}, strides[3] = {row, 128, row * (uint64_t)S_max};
+    if (!dsa_host::encode_tensor_map(&sm, dt, 4, const_cast<uint16_t*>(kv), dims, strides, box, sw)) return DSA_ERR_CUDA;
   }
   static uint64_t seen[dsa_host::kMaxSetupDevices];
   if (dsa_host::needs_setup(seen, nullptr)) {
@@ -715,7 +716,7 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
       return DSA_ERR_CUDA;
     dsa_host::mark_setup(seen);
   }
-  int rc = dsa_host::launch_pairs(mla_shared_kernel, (unsigned)pairs, kThreads, kSmem, stream, q_map, pk, pv, sk, sv, p);
+  int rc = dsa_host::launch_pairs(mla_shared_kernel, (unsigned)pairs, kThreads, kSmem, stream, q_map, pm, sm, p);
   if (rc != DSA_OK) return rc;
   return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)pairs, 8), dim3(256), 0, stream, p, pairs);
 }

@@ -31,43 +31,17 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Arrivals on a barrier at a shared::cluster address. They order tcgen05 and TMA work (with the
+// tcgen05 fences, and through the transaction count), not ordinary memory: a release at cluster
+// scope costs several hundred cycles, so ordinary writes that the other CTA's MMA issue relies on
+// pay for it separately (cluster_fence on both sides).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void arrive_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
-               : "memory");
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t phase) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(phase)
-      : "memory");
-  return ok != 0;
-}
-
-// mbar_wait for barriers that the other CTA arrives on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t phase, volatile int* abort_flag, int* status,
-                                                  int site) {
-  if (mbar_try_wait_cluster(bar, phase)) return true;
-  const uint64_t t0 = global_timer_ns();
-  uint64_t waited = 0;
-  for (uint32_t i = 1; i < kSpinLimit; ++i) {
-    if (mbar_try_wait_cluster(bar, phase)) return true;
-    if (abort_flag && *abort_flag) return false;
-    if (i % kPollsPerCheck == 0) {
-      waited = global_timer_ns() - t0;
-      if (waited > kWaitLimitNs) break;
-    }
-  }
-  record_timeout(status, site, waited);
-  if (abort_flag) *abort_flag = 1;
-  return false;
-}
+__device__ __forceinline__ void cluster_fence() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 // Loads into this CTA's shared memory whose bytes complete on the leader's barrier `bar` (a
 // shared::cluster address).
@@ -84,6 +58,14 @@ __device__ __forceinline__ void pair_load_3d(uint32_t dst, const CUtensorMap* ma
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void pair_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                             int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
 
