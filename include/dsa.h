@@ -421,6 +421,39 @@ DSA_API int dsa_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, con
 DSA_API size_t dsa_mla_shared_workspace_size(int B, int T, int P, int S_max);
 
 /*
+ * dsa_mla_weights - the attention weight that each cached row gets from each query, summed over the
+ * 128 heads, and its sum over the queries.
+ *
+ *   q       bf16 [B][T][128][576], kv bf16 [B][S_max][576], q_pos int32 [B][T], kv_len int32 [B]:
+ *           as dsa_mla_shared's own rows (query (b, t) sees s <= q_pos[b][t], s < kv_len[b])
+ *   lse     fp32 [B][T][128]: what the attention returned for these queries; over a cache in several
+ *           parts (a prefix and own rows) each part is one call with the lse of the whole
+ *   w       fp32 [B][T][ld], ld >= S_max, a multiple of 4: w[b][t][s] = sum over the heads of
+ *           exp(softmax_scale * q . kv[b][s] - lse) for visible rows, 0 for the others up to S_max
+ *           (entries from S_max to ld are left as they were)
+ *   acc, acc_out  fp32 [B][S_max], or both NULL: acc_out[b][s] = acc[b][s] + sum over t of w[b][t][s],
+ *           added in the order of t (the same bits every time); acc_out may be acc
+ * Rows that a query does not see may hold anything. B, T, S_max >= 1; B <= 65535; B * T <= 2^23;
+ * S_max at most DSA_MAX_POS; pointers 16-byte aligned.
+ */
+DSA_API int dsa_mla_weights(const uint16_t* q, const uint16_t* kv, const float* lse, const int32_t* q_pos,
+                            const int32_t* kv_len, int B, int T, int S_max, float softmax_scale, float* w, int64_t ld,
+                            const float* acc, float* acc_out, dsa_stream_t stream);
+
+/*
+ * dsa_mla_weights_selected - the same for sparse attention: the weight of each selected position,
+ * with the idx given to dsa_sparse_mla and the lse it returned.
+ *   idx     int32 [B][T][k]   selected positions, distinct within a query (-1 = unused slot, anywhere)
+ *   w       fp32 [B][T][ld], ld >= k, a multiple of 4: the weight of slot u, 0 for an unused one
+ *   acc, acc_out  as above: acc_out[b][idx] = acc[b][idx] + the weights of every query that selected it
+ * An idx >= S_max sets DSA_ERR_DEVICE_BOUNDS and counts as unused. 1 <= k <= DSA_MAX_POS; the rest as
+ * dsa_mla_weights.
+ */
+DSA_API int dsa_mla_weights_selected(const uint16_t* q, const uint16_t* kv, const int32_t* idx, const float* lse, int B,
+                                     int T, int S_max, int k, float softmax_scale, float* w, int64_t ld,
+                                     const float* acc, float* acc_out, dsa_stream_t stream);
+
+/*
  * dsa_cache_evict - cuts every sequence's cache back to at most `keep` rows, by the attention
  * weight that its rows have collected (dsa_mla_weights), in place.
  *
@@ -486,6 +519,10 @@ DSA_API int dsa_get_device_status(dsa_stream_t stream);
 #define DSA_SITE_SHARED_S 0x54          /* shared prefix: softmax waits for a score tile         */
 #define DSA_SITE_SHARED_P 0x55          /* shared prefix: MMA waits for probabilities            */
 #define DSA_SITE_SHARED_O 0x56          /* shared prefix: output waits for P V, or P V for it    */
+#define DSA_SITE_WEIGHTS_Q 0x61         /* attention weights: MMA waits for the query (TMA)      */
+#define DSA_SITE_WEIGHTS_FULL 0x62      /* attention weights: MMA waits for a block of keys      */
+#define DSA_SITE_WEIGHTS_EMPTY 0x63     /* attention weights: loads wait for free shared memory  */
+#define DSA_SITE_WEIGHTS_ACC 0x64       /* attention weights: scores, or room for them           */
 
 /*
  * dsa_get_error_detail - the detail recorded with the last non-OK code that

@@ -20,6 +20,7 @@ __all__ = [
     "dsa_sparse_mla_heads_workspace_size",
     "dsa_index_scores_paged", "dsa_sparse_mla_paged", "dsa_mla_q_absorb", "dsa_mla_kv_entry",
     "dsa_mla_out_absorb", "dsa_rope_freqs", "dsa_rope", "dsa_mla_shared", "dsa_mla_shared_workspace_size",
+    "dsa_mla_weights", "dsa_mla_weights_selected",
     "dsa_cache_evict", "dsa_cache_evict_workspace_size", "DSA_F16", "DSA_ROPE_INTERLEAVED", "DSA_ROPE_INVERSE",
     "dsa_sparse_mla_noalloc_scratch_bytes", "dsa_get_device_status", "dsa_get_error_detail",
     "dsa_selftest_wait_timeout", "dsa_status_string", "dsa_device_supported", "dsa_version",
@@ -48,6 +49,7 @@ SITE_NAMES = {
     0x31: "selftest", 0x41: "absorb:w", 0x42: "absorb:a_full", 0x43: "absorb:a_empty",
     0x44: "absorb:acc_full", 0x45: "absorb:acc_empty",
     0x51: "shared:q", 0x52: "shared:full", 0x53: "shared:empty", 0x54: "shared:s", 0x55: "shared:p", 0x56: "shared:o",
+    0x61: "weights:q", 0x62: "weights:full", 0x63: "weights:empty", 0x64: "weights:acc",
 }
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -91,6 +93,8 @@ def _load():
     L.dsa_mla_shared.argtypes = [vp, vp, i32, vp, vp, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]
     L.dsa_mla_shared_workspace_size.argtypes = [i32, i32, i32, i32]
     L.dsa_mla_shared_workspace_size.restype = sz
+    L.dsa_mla_weights.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, f32, vp, i64, vp, vp, vp]
+    L.dsa_mla_weights_selected.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, i64, vp, vp, vp]
     L.dsa_cache_evict.argtypes = [vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     L.dsa_cache_evict_workspace_size.argtypes = [i32, i32, i32]
     L.dsa_cache_evict_workspace_size.restype = sz
@@ -109,7 +113,7 @@ def _load():
               "dsa_sparse_mla_heads",
               "dsa_sparse_mla_noalloc", "dsa_get_device_status", "dsa_get_error_detail",
               "dsa_selftest_wait_timeout", "dsa_device_supported", "dsa_rope_freqs", "dsa_rope", "dsa_mla_shared",
-              "dsa_cache_evict"):
+              "dsa_mla_weights", "dsa_mla_weights_selected", "dsa_cache_evict"):
         getattr(L, f).restype = ctypes.c_int
     return L
 
@@ -674,6 +678,72 @@ def dsa_mla_shared(q, prefix, kv=None, q_pos=None, kv_len=None, softmax_scale: f
                                  float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_len, s)
     _check(rc, "dsa_mla_shared")
     return out, lse
+
+
+def _weights_args(q, kv, lse, acc, acc_out, w, width, others):
+    """Shape checks common to the two weight calls -> (B, T, S, acc_out)."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 4 or tuple(q.shape[2:]) != (128, 576):
+        raise ValueError(f"q must be [B, T, 128, 576], got {list(q.shape)}")
+    _need(kv, torch.bfloat16, "kv")
+    if kv.dim() != 3:
+        raise ValueError(f"kv must be [B, S_max, 576], got {list(kv.shape)}")
+    (B, T), S = q.shape[:2], kv.shape[1]
+    _shape(kv, (B, S, 576), "kv")
+    _need(lse, torch.float32, "lse")
+    _shape(lse, (B, T, 128), "lse")
+    if acc is None and acc_out is not None:
+        raise ValueError("acc_out needs acc")
+    acc_out = acc if acc_out is None else acc_out
+    for t, n in ((acc, "acc"), (acc_out, "acc_out")):
+        if t is not None:
+            _need(t, torch.float32, n)
+            _shape(t, (B, S), n)
+    width = S if width is None else width
+    if w is not None:
+        _need(w, torch.float32, "w")
+        if w.dim() != 3 or tuple(w.shape[:2]) != (B, T) or w.shape[2] < width or w.shape[2] % 4:
+            raise ValueError(f"w must be [{B}, {T}, ld], ld >= {width} and a multiple of 4, got {list(w.shape)}")
+    _one_device(q, kv=kv, lse=lse, acc=acc, acc_out=acc_out, w=w, **others)
+    return B, T, S, acc_out
+
+
+def dsa_mla_weights(q, kv, lse, q_pos, kv_len, softmax_scale: float = MLA_SOFTMAX_SCALE, acc=None, acc_out=None, w=None,
+                    stream=None):
+    """The attention weight of each visible row, summed over the heads: q bf16 [B,T,128,576], kv bf16 [B,S,576], lse
+    fp32 [B,T,128] from the attention, q_pos i32 [B,T], kv_len i32 [B] -> (w fp32 [B,T,ld], acc). w is 0 at rows a
+    query does not see; ld is S rounded up to 4. acc fp32 [B,S] grows by the queries' weights, in place unless acc_out
+    is given (None: not wanted)."""
+    B, T, S, acc_out = _weights_args(q, kv, lse, acc, acc_out, w, None, dict(q_pos=q_pos, kv_len=kv_len))
+    for t, n, shape in ((q_pos, "q_pos", (B, T)), (kv_len, "kv_len", (B,))):
+        _need(t, torch.int32, n)
+        _shape(t, shape, n)
+    with _on(q.device, stream) as s:
+        if w is None:
+            w = torch.empty((B, T, (S + 3) // 4 * 4), dtype=torch.float32, device=q.device)
+        rc = _lib.dsa_mla_weights(_ptr(q), _ptr(kv), _ptr(lse), _ptr(q_pos), _ptr(kv_len), B, T, S, float(softmax_scale),
+                                  _ptr(w), w.shape[2], _ptr(acc), _ptr(acc_out), s)
+    _check(rc, "dsa_mla_weights")
+    return w, acc_out
+
+
+def dsa_mla_weights_selected(q, kv, idx, lse, softmax_scale: float = MLA_SOFTMAX_SCALE, acc=None, acc_out=None, w=None,
+                             stream=None):
+    """dsa_mla_weights for sparse attention: idx i32 [B,T,k] as given to dsa_sparse_mla (-1: unused slot), lse as it
+    returned it -> (w fp32 [B,T,ld], acc); w[..., u] is the weight of slot u, ld is k rounded up to 4."""
+    _need(idx, torch.int32, "idx")
+    if idx.dim() != 3:
+        raise ValueError(f"idx must be [B, T, k], got {list(idx.shape)}")
+    k = idx.shape[2]
+    B, T, S, acc_out = _weights_args(q, kv, lse, acc, acc_out, w, k, dict(idx=idx))
+    _shape(idx, (B, T, k), "idx")
+    with _on(q.device, stream) as s:
+        if w is None:
+            w = torch.empty((B, T, (k + 3) // 4 * 4), dtype=torch.float32, device=q.device)
+        rc = _lib.dsa_mla_weights_selected(_ptr(q), _ptr(kv), _ptr(idx), _ptr(lse), B, T, S, k, float(softmax_scale),
+                                           _ptr(w), w.shape[2], _ptr(acc), _ptr(acc_out), s)
+    _check(rc, "dsa_mla_weights_selected")
+    return w, acc_out
 
 
 def dsa_cache_evict_workspace_size(B: int, S_max: int, keep: int) -> int:

@@ -602,6 +602,40 @@ int dsa_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const uint1
                                 ws_bytes, (cudaStream_t)stream, status);
 }
 
+static int mla_weights_checked(const uint16_t* q, const uint16_t* kv, const int32_t* idx, const float* lse,
+                               const int32_t* q_pos, const int32_t* kv_len, int B, int T, int S_max, int k, int64_t width,
+                               float softmax_scale, float* w, int64_t ld, const float* acc, float* acc_out,
+                               dsa_stream_t stream) {
+  if (B < 1 || B > 65535 || T < 1 || (int64_t)B * T > (1 << 23) || S_max < 1 || S_max > DSA_MAX_POS || width < 1 ||
+      width > DSA_MAX_POS || ld < width || (ld & 3) != 0 || ld > ((int64_t)1 << 31) || !(softmax_scale > 0.f) ||
+      !isfinite(softmax_scale) || (acc == nullptr) != (acc_out == nullptr) || !q || !kv || !lse || !w)
+    return DSA_ERR_INVALID_ARG;
+  const void* ptrs[] = {q, kv, idx, lse, q_pos, kv_len, w, acc, acc_out};
+  for (const void* p : ptrs)
+    if (!dsa_host::aligned16(p)) return DSA_ERR_INVALID_ARG;
+  int* status;
+  int rc = prologue(&status);
+  if (rc != DSA_OK) return rc;
+  return dsa::launch_mla_weights(q, kv, idx, lse, q_pos, kv_len, B, T, S_max, k, softmax_scale, w, ld, acc, acc_out,
+                                 (cudaStream_t)stream, status);
+}
+
+int dsa_mla_weights(const uint16_t* q, const uint16_t* kv, const float* lse, const int32_t* q_pos, const int32_t* kv_len,
+                    int B, int T, int S_max, float softmax_scale, float* w, int64_t ld, const float* acc, float* acc_out,
+                    dsa_stream_t stream) {
+  if (!q_pos || !kv_len) return DSA_ERR_INVALID_ARG;
+  return mla_weights_checked(q, kv, nullptr, lse, q_pos, kv_len, B, T, S_max, 0, S_max, softmax_scale, w, ld, acc, acc_out,
+                             stream);
+}
+
+int dsa_mla_weights_selected(const uint16_t* q, const uint16_t* kv, const int32_t* idx, const float* lse, int B, int T,
+                             int S_max, int k, float softmax_scale, float* w, int64_t ld, const float* acc, float* acc_out,
+                             dsa_stream_t stream) {
+  if (!idx) return DSA_ERR_INVALID_ARG;
+  return mla_weights_checked(q, kv, idx, lse, nullptr, nullptr, B, T, S_max, k, k, softmax_scale, w, ld, acc, acc_out,
+                             stream);
+}
+
 static bool evict_shape_ok(int B, int S_max, int keep) {
   return B >= 1 && B <= 65535 && S_max >= 1 && S_max <= DSA_MAX_POS && keep >= 1;
 }

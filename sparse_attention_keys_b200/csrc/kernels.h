@@ -61,6 +61,11 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
                       const int32_t* kv_len, int B, int T, int S_max, float softmax_scale, uint16_t* out, float* lse,
                       void* workspace, size_t ws_bytes, cudaStream_t stream, int* status);
 
+// idx NULL: dense over the visible rows (q_pos, kv_len); acc and acc_out NULL: no sum over the queries
+int launch_mla_weights(const uint16_t* q, const uint16_t* kv, const int32_t* idx, const float* lse, const int32_t* q_pos,
+                       const int32_t* kv_len, int B, int T, int S_max, int k, float softmax_scale, float* w, int64_t ld,
+                       const float* acc, float* acc_out, cudaStream_t stream, int* status);
+
 size_t cache_evict_workspace_size(int B, int S_max, int keep);
 int launch_cache_evict(const float* acc, const int32_t* pos, const int32_t* kv_len, int B, int S_max, int keep, int recent,
                        int sinks, uint16_t* kv, uint8_t* k8, float* k_scale, float* acc_out, int32_t* pos_out,

@@ -1,0 +1,460 @@
+// dsa_mla_weights, dsa_mla_weights_selected: the attention weight that each cached position gets,
+// summed over the heads, and added up over the queries.
+//
+// w[b][t][s] = sum_h exp(scale * q[b][t][h] . kv[b][s] - lse[b][t][h]) with the lse that the
+// attention returned, for the visible rows (dense) or for the selected ones (w[b][t][u] for slot u).
+//
+// The scores are computed transposed, S^T = K Q^T, so that a TMEM lane holds one key and the 128
+// columns its heads: the sum over the heads stays inside a thread. One CTA per SM takes an equal
+// share of all (query, 128-key tile) pairs; the query (128 x 576, 144 KB) stays in shared memory while
+// 16 KB blocks of keys (128 keys x 64 features) pass through a ring of five. Per tile 36 MMAs of
+// 128 x 128 x 16 (65 cycles each, 2340) into one of four 128-column accumulators, and 128 x 128
+// exponentials (1024 cycles of MUFU). For one query per sequence HBM is the bound: 147 KB per tile
+// take an SM's share of it 6300 cycles.
+//
+// Selected rows are gathered by four warps with 16-byte cp.async into the swizzled operand layout,
+// 128 bytes of each row per block; the whole rows of the next tile are hinted into L2 one tile
+// ahead, so that DRAM sees 1152-byte requests.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kernels.h"
+#include "pair.cuh"
+
+namespace dsa {
+
+namespace {
+
+constexpr int kHeads = 128, kDqk = 576, kTile = 128;
+constexpr int kBlock = 128 * 128;                  // 16 KB: 64 features of 128 rows
+constexpr int kSlots = 5;
+constexpr int kOffRing = 9 * kBlock;
+constexpr int kOffBar = kOffRing + kSlots * kBlock;
+constexpr int kOffLse = kOffBar + 256;             // 2 x 128 fp32
+constexpr int kOffScan = kOffLse + 2 * 128 * 4;    // set-up words
+constexpr int kSmem = 1024 + kOffScan + 256;
+static_assert(kSmem <= 232448, "shared memory per CTA");
+constexpr int kAccs = 4;                           // accumulators of 128 columns
+constexpr int kGatherWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+
+}  // namespace
+
+struct WeightsParams {
+  const uint16_t* kv;
+  const int32_t* idx;      // [B][T][k] (selected rows), or NULL (dense)
+  const float* lse;        // [B][T][128]
+  const int32_t* q_pos;    // dense only
+  const int32_t* kv_len;
+  int64_t BT;
+  int T, S_max, k;
+  int64_t ld;
+  float scale_log2;
+  float* w;
+  const float* acc;
+  float* acc_out;
+  int* status;
+};
+
+namespace {
+
+// keys (or slots) of query `tok`
+__device__ __forceinline__ int keys_of(const WeightsParams& p, int64_t tok) {
+  if (p.idx) return p.k;
+  const int64_t v = (int64_t)__ldg(p.q_pos + tok) + 1;
+  const int64_t n = __ldg(p.kv_len + tok / p.T);
+  return (int)max((int64_t)0, min(min(v, n), (int64_t)p.S_max));
+}
+__device__ __forceinline__ int tiles_of(const WeightsParams& p, int64_t tok) {
+  return (keys_of(p, tok) + kTile - 1) / kTile;
+}
+
+// The runs of tiles [t0, t1) of one query each that make up this CTA's range.
+struct Runs {
+  int64_t left, tok;
+  int t0, t1, keys;
+  __device__ __forceinline__ void settle(const WeightsParams& p) {
+    while (left > 0) {
+      keys = keys_of(p, tok);
+      const int tiles = (keys + kTile - 1) / kTile;
+      if (tiles > t0) {
+        t1 = (int)min((int64_t)tiles, t0 + left);
+        return;
+      }
+      ++tok;
+      t0 = 0;
+    }
+  }
+  __device__ __forceinline__ void start(const WeightsParams& p, int64_t t, int64_t off, int64_t count) {
+    tok = t;
+    t0 = (int)off;
+    left = count;
+    settle(p);
+  }
+  __device__ __forceinline__ void next(const WeightsParams& p) {
+    left -= t1 - t0;
+    ++tok;
+    t0 = 0;
+    settle(p);
+  }
+};
+
+}  // namespace
+
+template <bool SELECTED>
+__global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
+    mla_weights_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                       const WeightsParams p) {
+  constexpr int kThreads = SELECTED ? 384 : 256;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* full = bars;                 // [kSlots] keys landed
+  uint64_t* empty = full + kSlots;       // [kSlots] their MMAs are done
+  uint64_t* acc_full = empty + kSlots;   // [kAccs] scores ready
+  uint64_t* acc_empty = acc_full + kAccs;  // [kAccs] scores read
+  uint64_t* q_full = acc_empty + kAccs;
+  uint64_t* q_empty = q_full + 1;        // the run's MMAs are done
+  float* lse_sh = reinterpret_cast<float*>(smem + kOffLse);
+  long long* scan_sh = reinterpret_cast<long long*>(smem + kOffScan);       // [kThreads / 32]
+  long long* start_sh = scan_sh + 16;                                       // first query, tile of it
+  uint32_t& tmem_base_sh = *reinterpret_cast<uint32_t*>(start_sh + 2);
+  int& abort_flag = *reinterpret_cast<int*>(start_sh + 3);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&full[s], SELECTED ? kGatherWarps * 32 : 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < kAccs; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    fence_barrier_init();
+    start_sh[0] = start_sh[1] = 0;
+  }
+  if (warp == 2) {
+    tmem_alloc(&tmem_base_sh, 512);
+    tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // this CTA's share: thread i sums the tiles of the queries [i * per, (i + 1) * per)
+  const int64_t per = (p.BT + kThreads - 1) / kThreads;
+  const int64_t ua = min(p.BT, tid * per), ub = min(p.BT, ua + per);
+  long long sum = 0;
+  for (int64_t u = ua; u < ub; ++u) sum += tiles_of(p, u);
+  long long pre = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, pre, d);
+    if (lane >= d) pre += o;
+  }
+  if (lane == 31) scan_sh[warp] = pre;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0, base = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w == warp) base = total;
+    total += scan_sh[w];
+  }
+  const long long excl = base + pre - sum;
+  const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+  if (sum > 0 && lo >= excl && lo < excl + sum) {
+    long long off = lo - excl;
+    int64_t u = ua;
+    for (; u < ub; ++u) {
+      const int n = tiles_of(p, u);
+      if (off < n) break;
+      off -= n;
+    }
+    start_sh[0] = u;
+    start_sh[1] = off;
+  }
+  __syncthreads();
+  const uint32_t tmem = tmem_base_sh;
+  const uint32_t ring = smem_u32(smem + kOffRing);
+  Runs r;
+  r.start(p, start_sh[0], start_sh[1], hi - lo);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA: queries, and dense keys
+    if (elect_one()) {
+      int slot = 0, run = 0;
+      uint32_t ph = 1;                   // a fresh slot counts as freed
+      bool ok = true;
+      for (; ok && r.left > 0; r.next(p), ++run) {
+        if (run > 0 && !mbar_wait(q_empty, (run + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY)) break;
+        mbar_arrive_expect_tx(q_full, 9 * kBlock);
+        for (int f = 0; f < 9; ++f) tma_load_2d(smem + f * kBlock, &q_map, q_full, 64 * f, (int32_t)(r.tok * kHeads));
+        if (SELECTED) continue;
+        const int b = (int)(r.tok / p.T);
+        for (int t = r.t0; ok && t < r.t1; ++t)
+          for (int f = 0; f < 9; ++f) {
+            if (!mbar_wait(&empty[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[slot], kBlock);
+            tma_load_3d(smem + kOffRing + slot * kBlock, &k_map, &full[slot], 64 * f, t * kTile, b);
+            if (++slot == kSlots) {
+              slot = 0;
+              ph ^= 1;
+            }
+          }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issue
+    if (elect_one()) {
+      const uint32_t idesc = idesc_f32acc(1, 1, 128, kHeads, 0, 0);
+      const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(ring);
+      int slot = 0, run = 0;
+      uint32_t ph = 0, g = 0;
+      bool ok = true;
+      for (; ok && r.left > 0; r.next(p), ++run) {
+        if (!mbar_wait(q_full, run & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_Q)) break;
+        tc_fence_after();
+        for (int t = r.t0; ok && t < r.t1; ++t, ++g) {
+          if (!mbar_wait(&acc_empty[g % kAccs], ((g / kAccs) + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + (g % kAccs) * kHeads;
+#pragma unroll 1
+          for (int f = 0; f < 9; ++f) {
+            if (!mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL)) {
+              ok = false;
+              break;
+            }
+            if (SELECTED) fence_proxy_async_smem();      // cp.async writes -> MMA reads
+            tc_fence_after();
+            const uint64_t a = k_desc + (uint64_t)((slot * kBlock) >> 4), b = q_desc + (uint64_t)((f * kBlock) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_f16_ss(d, a + 2 * k, b + 2 * k, idesc, (f | k) != 0);
+            mma_commit(&empty[slot]);
+            if (++slot == kSlots) {
+              slot = 0;
+              ph ^= 1;
+            }
+          }
+          if (ok) mma_commit(&acc_full[g % kAccs]);
+        }
+        if (ok) mma_commit(q_empty);
+      }
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ gather (selected rows)
+    // warp v copies rows 32 v .. 32 v + 31 of the tile: lane i holds the row number of row 32 v + i
+    const int v = warp - 8;
+    int slot = 0;
+    uint32_t ph = 1;
+    bool ok = true;
+    for (; ok && r.left > 0; r.next(p)) {
+      const uint16_t* kv = p.kv + r.tok / p.T * p.S_max * kDqk;
+      const int32_t* idx = p.idx + r.tok * p.k;
+      auto row_of = [&](int t) {
+        const int u = t * kTile + 32 * v + lane;
+        const int row = t < r.t1 && u < p.k ? __ldg(idx + u) : -1;
+        if (row >= p.S_max) set_status(p.status, DSA_ERR_DEVICE_BOUNDS);
+        return row < p.S_max ? row : -1;
+      };
+      auto hint = [&](int row) {
+        if (row >= 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(kv + (int64_t)row * kDqk), "r"(kDqk * 2) : "memory");
+      };
+      int row = row_of(r.t0);
+      hint(row);
+      for (int t = r.t0; ok && t < r.t1; ++t) {
+        const int next = row_of(t + 1);
+        hint(next);
+        for (int f = 0; f < 9; ++f) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY))) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = ring + slot * kBlock;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // four rows per step, eight 16-byte chunks each; rows that take no part are zeros
+            const int rr = 4 * i + (lane >> 3), c = lane & 7;
+            const int src = __shfl_sync(0xffffffffu, row, rr);
+            const int at = 32 * v + rr;
+            cp_async_16_zfill(dst + at * 128 + ((c ^ (at & 7)) << 4), kv + (int64_t)max(src, 0) * kDqk + 64 * f + 8 * c,
+                              src >= 0);
+          }
+          cp_async_mbar_arrive(&full[slot]);
+          if (++slot == kSlots) {
+            slot = 0;
+            ph ^= 1;
+          }
+        }
+        row = next;
+      }
+    }
+    cp_async_wait_all();
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ exponentials, one thread per key
+    const int key = tid - 128;
+    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    uint32_t g = 0;
+    int run = 0;
+    bool ok = true;
+    for (; ok && r.left > 0; r.next(p), ++run) {
+      float* ls = lse_sh + (run & 1) * kHeads;
+      ls[key] = __ldg(p.lse + r.tok * kHeads + key) * kLog2e;
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      for (int t = r.t0; ok && t < r.t1; ++t, ++g) {
+        const int u = t * kTile + key;
+        bool take = u < r.keys;
+        if (SELECTED && take) {
+          const int row = __ldg(p.idx + r.tok * p.k + u);
+          take = row >= 0 && row < p.S_max;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[g % kAccs], (g / kAccs) & 1, &abort_flag, p.status,
+                                               DSA_SITE_WEIGHTS_ACC))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t x[2][32];
+        const uint32_t d = t_row + (g % kAccs) * kHeads;
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          tmem_ld32(d + 32 * c, x[0]);
+          tmem_ld32(d + 32 * c + 32, x[1]);
+          tmem_ld_wait();
+          if (c == 2) {                  // the scores are in registers: the accumulator may be overwritten
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[g % kAccs]);
+          }
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(ls + 32 * c + i);
+            const uint32_t* y = &x[i >> 5][i & 31];
+            s4[0] += exp2_approx(fmaf(__uint_as_float(y[0]), p.scale_log2, -l4.x));
+            s4[1] += exp2_approx(fmaf(__uint_as_float(y[1]), p.scale_log2, -l4.y));
+            s4[2] += exp2_approx(fmaf(__uint_as_float(y[2]), p.scale_log2, -l4.z));
+            s4[3] += exp2_approx(fmaf(__uint_as_float(y[3]), p.scale_log2, -l4.w));
+          }
+        }
+        if (u < r.keys) p.w[r.tok * p.ld + u] = take ? (s4[0] + s4[1]) + (s4[2] + s4[3]) : 0.f;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// Dense: zeros behind each query's keys, and acc_out = acc + the weights of the queries in their order.
+__global__ void __launch_bounds__(256) mla_weights_sum_kernel(const WeightsParams p) {
+  const int64_t b = blockIdx.y;
+  const int s = blockIdx.x * 256 + threadIdx.x;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (s >= p.S_max) return;
+  float a = p.acc_out ? p.acc[b * p.S_max + s] : 0.f;
+  float* w = p.w + b * p.T * p.ld + s;
+  for (int t = 0; t < p.T; ++t) {
+    if (s < keys_of(p, b * p.T + t)) a += p.acc_out ? w[t * p.ld] : 0.f;
+    else w[t * p.ld] = 0.f;
+  }
+  if (p.acc_out) p.acc_out[b * p.S_max + s] = a;
+}
+
+// Selected: acc_out = acc + the weights of the queries in their order; a block holds kRange positions of
+// one sequence in shared memory. Positions of one query are distinct, so no two threads meet.
+constexpr int kRange = 4096;
+__global__ void __launch_bounds__(1024) mla_weights_scatter_kernel(const WeightsParams p) {
+  __shared__ float a[kRange];
+  const int64_t b = blockIdx.y;
+  const int s0 = blockIdx.x * kRange, n = min(kRange, p.S_max - s0);
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int i = threadIdx.x; i < n; i += 1024) a[i] = p.acc[b * p.S_max + s0 + i];
+  __syncthreads();
+  for (int t = 0; t < p.T; ++t) {
+    const int64_t q = b * p.T + t;
+    for (int u = threadIdx.x; u < p.k; u += 1024) {
+      const int i = __ldg(p.idx + q * p.k + u) - s0;
+      if (i >= 0 && i < n) a[i] += p.w[q * p.ld + u];
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += 1024) p.acc_out[b * p.S_max + s0 + i] = a[i];
+}
+
+namespace {
+
+template <bool SELECTED>
+int launch_weights(const uint16_t* q, const WeightsParams& p, int64_t B, cudaStream_t stream) {
+  const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  CUtensorMap q_map, k_map;
+  const uint64_t row = kDqk * 2;
+  if (!dsa_host::encode_tensor_map_2d(&q_map, dt, const_cast<uint16_t*>(q), kDqk, (uint64_t)p.BT * kHeads, row, 64, kHeads,
+                                      sw))
+    return DSA_ERR_CUDA;
+  k_map = q_map;
+  if (!SELECTED) {
+    const uint64_t dims[3] = {(uint64_t)kDqk, (uint64_t)p.S_max, (uint64_t)B};
+    const uint64_t strides[2] = {row, row * (uint64_t)p.S_max};
+    const uint32_t box[3] = {64, kTile, 1};
+    if (!dsa_host::encode_tensor_map_3d(&k_map, dt, const_cast<uint16_t*>(p.kv), dims, strides, box, sw)) return DSA_ERR_CUDA;
+  }
+  static uint64_t seen[dsa_host::kMaxSetupDevices];
+  if (dsa_host::needs_setup(seen, nullptr)) {
+    if (cudaFuncSetAttribute(mla_weights_kernel<SELECTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
+      return DSA_ERR_CUDA;
+    dsa_host::mark_setup(seen);
+  }
+  const int64_t tiles = p.BT * (((SELECTED ? p.k : p.S_max) + kTile - 1) / kTile);
+  const unsigned grid = (unsigned)std::min<int64_t>(dsa_host::device_sm_count(), tiles);
+  const int rc = dsa_host::launch(mla_weights_kernel<SELECTED>, dim3(grid), dim3(SELECTED ? 384 : 256), kSmem, stream, q_map,
+                                  k_map, p);
+  if (rc != DSA_OK) return rc;
+  if (!SELECTED)
+    return dsa_host::launch(mla_weights_sum_kernel, dim3((unsigned)((p.S_max + 255) / 256), (unsigned)B), dim3(256), 0, stream, p);
+  if (!p.acc_out) return DSA_OK;
+  return dsa_host::launch(mla_weights_scatter_kernel, dim3((unsigned)((p.S_max + kRange - 1) / kRange), (unsigned)B),
+                          dim3(1024), 0, stream, p);
+}
+
+}  // namespace
+
+int launch_mla_weights(const uint16_t* q, const uint16_t* kv, const int32_t* idx, const float* lse, const int32_t* q_pos,
+                       const int32_t* kv_len, int B, int T, int S_max, int k, float softmax_scale, float* w, int64_t ld,
+                       const float* acc, float* acc_out, cudaStream_t stream, int* status) {
+  WeightsParams p = {};
+  p.kv = kv;
+  p.idx = idx;
+  p.lse = lse;
+  p.q_pos = q_pos;
+  p.kv_len = kv_len;
+  p.BT = (int64_t)B * T;
+  p.T = T;
+  p.S_max = S_max;
+  p.k = k;
+  p.ld = ld;
+  p.scale_log2 = softmax_scale * kLog2e;
+  p.w = w;
+  p.acc = acc;
+  p.acc_out = acc_out;
+  p.status = status;
+  return idx ? launch_weights<true>(q, p, B, stream) : launch_weights<false>(q, p, B, stream);
+}
+
+}  // namespace dsa

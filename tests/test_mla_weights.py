@@ -1,0 +1,302 @@
+"""dsa_mla_weights and dsa_mla_weights_selected: head-summed attention weights against the formula in 64
+bits, and the whole loop they belong to.
+
+Tolerance. A score is off by d = 576 * 2^-24 * scale * sum |q k| (fp32 accumulation of exact products),
+its base-2 exponent by two roundings of 2^-24 of |z| and |lse| (each times log2 e in fp32), the approximate
+exponential by 2^-21, the sum over 128 heads by 2^-17: |dw| <= sum_h p (d + 2^-22 (|z| + |lse|) + 2^-16)
+(p grows with e^d: 2 d is taken). A sum over T queries adds T 2^-24 of itself."""
+import ctypes
+
+import pytest
+import torch
+
+import __graft_entry__
+
+__graft_entry__._build_module().build()
+import sparse_attention_keys_b200 as dsa  # noqa: E402
+
+gpu = pytest.mark.gpu
+SCALE = dsa.MLA_SOFTMAX_SCALE
+
+
+def test_abi_refusals():
+    p, odd, n = ctypes.c_void_p(64), ctypes.c_void_p(65), None
+    f = ctypes.c_float
+    #        q kv lse q_pos kv_len B T S scale w ld acc acc_out stream
+    dense = [p, p, p, p, p, 2, 1, 64, f(0.1), p, 64, p, p, n]
+    #        q kv idx lse B T S k scale w ld acc acc_out stream
+    picked = [p, p, p, p, 2, 1, 64, 16, f(0.1), p, 16, p, p, n]
+
+    def bad(call, good, **kw):
+        a = list(good)
+        for i, v in kw.items():
+            a[int(i[1:])] = v
+        return call(*a)
+
+    def d(**kw):
+        return bad(dsa.lib.dsa_mla_weights, dense, **kw)
+
+    def s(**kw):
+        return bad(dsa.lib.dsa_mla_weights_selected, picked, **kw)
+
+    assert d(_5=0) == 1 and d(_5=65536) == 1 and d(_6=0) == 1 and d(_7=0) == 1 and d(_7=(1 << 20) + 1) == 1
+    assert d(_10=63) == 1 and d(_10=60) == 1 and d(_10=66) == 1 and d(_8=f(0.0)) == 1 and d(_8=f(float("inf"))) == 1
+    assert d(_11=n) == 1 and d(_12=n) == 1                          # a sum needs both
+    for i in (0, 1, 2, 3, 4, 9):
+        assert d(**{f"_{i}": n}) == 1 and d(**{f"_{i}": odd}) == 1
+    for i in (0, 1, 2, 3, 9):
+        assert s(**{f"_{i}": n}) == 1 and s(**{f"_{i}": odd}) == 1
+    assert s(_4=0) == 1 and s(_5=0) == 1 and s(_6=0) == 1 and s(_7=0) == 1 and s(_10=12) == 1 and s(_10=18) == 1
+    assert s(_5=1 << 23) == 1 and s(_11=odd) == 1 and s(_12=odd) == 1
+
+
+def test_binding_refusals():
+    q = torch.zeros(1, 1, 128, 576, dtype=torch.bfloat16)
+    lse = torch.zeros(1, 1, 128)
+    with pytest.raises(ValueError):                                 # host memory
+        dsa.dsa_mla_weights(q, q[0], lse, None, None)
+    with pytest.raises(TypeError):
+        dsa.dsa_mla_weights_selected(q, q[0], torch.zeros(1, 1, 4), lse)
+
+
+# ------------------------------------------------------------------------------------------- GPU
+def make(B, T, S, seed=0, lens=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    q = torch.randn((B, T, 128, 576), generator=g, device="cuda").bfloat16()
+    kv = torch.randn((B, S, 576), generator=g, device="cuda").bfloat16()
+    if lens is None:
+        lens = torch.randint(0, S + 1, (B,), generator=g, device="cuda")
+    kv_len = torch.as_tensor(lens, dtype=torch.int32, device="cuda")
+    q_pos = (kv_len[:, None] - T + torch.arange(T, device="cuda")).to(torch.int32)
+    return q, kv, q_pos, kv_len
+
+
+def reference(q, kv, lse, rows):
+    """rows: [B][T] lists of row indices -> ([B][T] weights, [B][T] tolerances) in float64"""
+    out = []
+    for b in range(q.shape[0]):
+        line = []
+        for t in range(q.shape[1]):
+            k = kv[b, rows[b][t]].double()
+            x = q[b, t].double()
+            z = SCALE * x @ k.t()
+            ls = lse[b, t].double()[:, None]
+            p = torch.exp(z - ls)
+            d = 576 * 2.0 ** -24 * SCALE * (x.abs() @ k.abs().t())
+            line.append((p.sum(0), (p * (2 * d + 2.0 ** -22 * (z.abs() + ls.abs()) + 2.0 ** -16)).sum(0)))
+        out.append(line)
+    return out
+
+
+def visible(q_pos, kv_len, S, b, t):
+    return max(0, min(int(q_pos[b, t]) + 1, int(kv_len[b]), S))
+
+
+def lse_of(q, kv, rows):
+    lse = torch.zeros(q.shape[:3], dtype=torch.float64, device="cuda")
+    for b in range(q.shape[0]):
+        for t in range(q.shape[1]):
+            lse[b, t] = torch.logsumexp(SCALE * q[b, t].double() @ kv[b, rows[b][t]].double().t(), -1)
+    return lse.float()
+
+
+def close(got, want, tol):
+    assert bool(((got.double() - want).abs() <= tol).all()), float(((got.double() - want).abs() - tol).max())
+
+
+@gpu
+@pytest.mark.parametrize("B,T,S", [(1, 1, 1), (2, 1, 127), (3, 1, 130), (5, 1, 1031), (1, 2, 5), (2, 3, 260), (1, 7, 128),
+                                   (200, 1, 40), (3, 40, 300)])
+def test_weights(B, T, S):
+    q, kv, q_pos, kv_len = make(B, T, S, seed=S)
+    rows = [[torch.arange(visible(q_pos, kv_len, S, b, t), device="cuda") for t in range(T)] for b in range(B)]
+    lse = lse_of(q, kv, rows)
+    acc = torch.rand((B, S), device="cuda")
+    ld = (S + 3) // 4 * 4 + 4
+    w = torch.full((B, T, ld), -3.0, device="cuda")
+    out = torch.empty_like(acc)
+    dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len, acc=acc, acc_out=out, w=w)
+    assert dsa.dsa_get_device_status() == 0
+    ref = reference(q, kv, lse, rows)
+    assert bool((w[..., S:] == -3.0).all())
+    for b in range(B):
+        total, slack = acc[b].double(), torch.zeros(S, dtype=torch.float64, device="cuda")
+        for t in range(T):
+            n = len(rows[b][t])
+            close(w[b, t, :n], *ref[b][t])
+            assert bool((w[b, t, n:S] == 0).all())
+            total[:n] += ref[b][t][0]
+            slack[:n] += ref[b][t][1]
+        close(out[b], total, slack + (T + 1) * 2.0 ** -24 * total)
+        assert T > 1 or abs(float(w[b, 0, :S].sum()) - (128 if len(rows[b][0]) else 0)) < 1e-2
+    # without a sum, and in place: the same bits
+    w2, none = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len)
+    assert none is None and torch.equal(w2[..., :S], w[..., :S])
+    dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len, acc=acc, w=w)
+    assert torch.equal(acc, out)
+
+
+@gpu
+def test_hidden_rows_lengths_and_minus_infinity():
+    lens = [0, 1, 128, 129, 256, 300, 77]
+    q, kv, q_pos, kv_len = make(7, 2, 256, seed=2, lens=lens)
+    q_pos[4] = torch.tensor([-5, 1 << 30])
+    rows = [[torch.arange(visible(q_pos, kv_len, 256, b, t), device="cuda") for t in range(2)] for b in range(7)]
+    lse = lse_of(q, kv, rows)                                      # -inf where nothing is seen
+    assert bool(lse[0].isinf().all())
+    clean, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len)
+    for b in range(7):
+        kv[b, len(rows[b][1]):] = float("nan")
+    got, acc = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len, acc=torch.zeros((7, 256), device="cuda"))
+    assert torch.equal(clean, got) and bool(acc.isfinite().all()) and torch.equal(acc, got.sum(1))
+    ref = reference(q, kv, lse, rows)
+    for b in range(7):
+        for t in range(2):
+            close(got[b, t, :len(rows[b][t])], *ref[b][t])
+            assert bool((got[b, t, len(rows[b][t]):] == 0).all())
+
+
+@gpu
+@pytest.mark.parametrize("B,T,S,k", [(1, 1, 1, 1), (3, 1, 700, 130), (2, 4, 300, 50), (1, 1, 20000, 2048), (70, 2, 90, 7),
+                                     (1, 60, 9000, 256)])
+def test_selected(B, T, S, k):
+    q, kv, _, _ = make(B, T, S, seed=k)
+    g = torch.Generator(device="cuda").manual_seed(k)
+    idx = torch.rand((B, T, S), generator=g, device="cuda").topk(min(k, S), -1).indices
+    idx = torch.nn.functional.pad(idx, (0, k - min(k, S)), value=-1).to(torch.int32)
+    holes = torch.rand((B, T, k), generator=g, device="cuda") < 0.2             # unused slots anywhere
+    holes[..., 0] = False
+    idx = torch.where(holes, -1, idx).contiguous()
+    rows = [[idx[b, t][idx[b, t] >= 0].long() for t in range(T)] for b in range(B)]
+    lse = lse_of(q, kv, rows)
+    acc = torch.rand((B, S), device="cuda")
+    w, out = dsa.dsa_mla_weights_selected(q, kv, idx, lse, acc=acc, acc_out=torch.empty_like(acc))
+    assert dsa.dsa_get_device_status() == 0
+    ref = reference(q, kv, lse, rows)
+    for b in range(B):
+        total, slack = acc[b].double(), torch.zeros(S, dtype=torch.float64, device="cuda")
+        for t in range(T):
+            close(w[b, t, :k][idx[b, t] >= 0], *ref[b][t])
+            assert bool((w[b, t, :k][idx[b, t] < 0] == 0).all())
+            total[rows[b][t]] += ref[b][t][0]
+            slack[rows[b][t]] += ref[b][t][1]
+        close(out[b], total, slack + (T + 1) * 2.0 ** -24 * total)
+    w2, _ = dsa.dsa_mla_weights_selected(q, kv, idx, lse, acc=acc)
+    assert torch.equal(acc, out) and torch.equal(w2[..., :k], w[..., :k])
+
+
+@gpu
+def test_selected_index_past_the_cache():
+    """It is recorded and counts as unused; NaN in rows that nobody selected stays there."""
+    q, kv, _, _ = make(1, 1, 64, seed=5)
+    idx = torch.arange(10, device="cuda", dtype=torch.int32)[None, None].contiguous()
+    kv[0, 10:] = float("nan")
+    lse = lse_of(q, kv, [[torch.arange(10, device="cuda")]])
+    want, a = dsa.dsa_mla_weights_selected(q, kv, idx, lse, acc=torch.zeros((1, 64), device="cuda"))
+    assert dsa.dsa_get_device_status() == 0 and bool((a[0, 10:] == 0).all())
+    idx2 = torch.cat([idx, torch.full((1, 1, 2), 64, dtype=torch.int32, device="cuda")], -1)
+    got, a2 = dsa.dsa_mla_weights_selected(q, kv, idx2, lse, acc=torch.zeros((1, 64), device="cuda"))
+    assert dsa.dsa_get_device_status() == 5
+    assert torch.equal(got[..., :10], want[..., :10]) and bool((got[..., 10:] == 0).all()) and torch.equal(a, a2)
+
+
+@gpu
+def test_streams_graphs_and_refusals():
+    q, kv, q_pos, kv_len = make(4, 1, 400, seed=6, lens=[400, 0, 130, 7])
+    out, lse = dsa.dsa_mla_shared(q, None, kv, q_pos, kv_len)
+    want, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    a, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len, stream=side)
+    b, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len)
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+    acc, w = torch.zeros((4, 400), device="cuda"), torch.empty_like(want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len, acc=acc, w=w)
+    for i in range(1, 4):
+        g.replay()
+        assert torch.equal(w, want)
+    assert bool((acc - 3 * want[:, 0]).abs().max() <= 3 * 2.0 ** -23 * acc.max())
+    good = dict(q=q, kv=kv, lse=lse, q_pos=q_pos, kv_len=kv_len)
+    for bad in (dict(q=q[:3]), dict(kv=kv[..., :512].contiguous()), dict(lse=lse[..., :64].contiguous()), dict(q_pos=q_pos[:3]),
+                dict(kv_len=kv_len.long()), dict(acc_out=acc), dict(acc=acc[:, :399].contiguous()), dict(w=w[..., :396].contiguous()),
+                dict(w=torch.empty((4, 1, 402), device="cuda")), dict(lse=lse.cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            dsa.dsa_mla_weights(**{**good, **bad})
+
+
+@gpu
+def test_cache_past_32_bit_offsets():
+    B, S = 4, 940000
+    kv = torch.zeros((B, S, 576), dtype=torch.bfloat16, device="cuda")
+    assert kv.numel() > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kv[3, -300:] = torch.randn((300, 576), generator=g, device="cuda").bfloat16()
+    q = torch.randn((B, 1, 128, 576), generator=g, device="cuda").bfloat16()
+    idx = (S - 300 + torch.randperm(300, device="cuda", generator=g)).to(torch.int32).expand(B, 1, 300).contiguous()
+    lse = torch.full((B, 1, 128), 9.0, device="cuda")
+    w, _ = dsa.dsa_mla_weights_selected(q, kv, idx, lse)
+    close(w[3, 0], *reference(q[3:], kv[3:], lse[3:], [[idx[3, 0].long()]])[0][0])
+
+
+@gpu
+def test_the_whole_loop():
+    """As a server runs it: two sequences behind one prompt decode with a budget of 40 own rows. The rotary key
+    enters the cache, attention runs over prompt and own rows, its lse gives the weights, and every eighth step
+    evicts. Checked against the same loop in float64 that follows the kernel's choice of rows."""
+    B, P, S, keep, steps = 2, 150, 48, 40, 30
+    g = torch.Generator(device="cuda").manual_seed(11)
+
+    def normal(*s):
+        return torch.randn(s, generator=g, device="cuda").bfloat16()
+
+    prefix, kv = normal(P, 576), torch.full((B, S, 576), float("nan"), dtype=torch.bfloat16, device="cuda")
+    k8 = torch.zeros((B, S, 128), dtype=torch.uint8, device="cuda")
+    ks = torch.zeros((B, S), device="cuda")
+    pos = torch.zeros((B, S), dtype=torch.int32, device="cuda")
+    acc = torch.zeros((B, S), device="cuda")
+    kv_len = torch.zeros(B, dtype=torch.int32, device="cuda")
+    freqs = dsa.dsa_rope_freqs(32, factor=40.0, original_len=4096).cuda()
+    held = [dict() for _ in range(B)]                                # position -> (row of the cache, weight)
+    for step in range(steps):
+        n = int(kv_len[0])
+        latent = normal(B, 576)
+        at = torch.full((B,), P + step, dtype=torch.int32, device="cuda")
+        kv[:, n] = dsa.dsa_rope(latent, at, freqs, offset=512, interleaved=True)
+        k8[:, n], ks[:, n], pos[:, n], acc[:, n] = step, float(step), step, 0.0
+        kv_len += 1
+        for b in range(B):
+            held[b][step] = [kv[b, n].double(), torch.zeros((), dtype=torch.float64, device="cuda")]
+        q = normal(B, 1, 128, 576)
+        q_pos = (kv_len[:, None] - 1).contiguous()
+        out, lse = dsa.dsa_mla_shared(q, prefix, kv, q_pos, kv_len)
+        w, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len, acc=acc)
+        for b in range(B):
+            rows = torch.stack([r for r, _ in held[b].values()])
+            keys = torch.cat([prefix.double(), rows])
+            p = torch.softmax(SCALE * q[b, 0].double() @ keys.t(), -1)
+            want = p @ keys[:, :512]
+            # bf16 weights and output: 2^-8 each, with room for the scores' 2^-9
+            assert bool(((out[b, 0].double() - want).abs() <= 2.0 ** -6 * (p @ keys[:, :512].abs())).all())
+            for h, x in zip(held[b].values(), p[:, P:].sum(0)):
+                h[1] += x
+        if int(kv_len[0]) == S:
+            dsa.dsa_cache_evict(acc, pos, kv_len, keep, recent=8, sinks=2, kv=kv, k8=k8, k_scale=ks)
+            for b in range(B):
+                alive = pos[b, :keep].tolist()
+                ranked = sorted(held[b], key=lambda s: (not (s > step - 8 or s < 2), -float(held[b][s][1])))
+                # the choice agrees up to weights that fp32 cannot tell apart
+                border = float(held[b][ranked[keep - 1]][1])
+                for s in set(alive) ^ set(ranked[:keep]):
+                    assert abs(float(held[b][s][1]) - border) <= 1e-4 * border
+                held[b] = {s: held[b][s] for s in alive}
+        for b in range(B):
+            m = int(kv_len[b])
+            order = pos[b, :m].tolist()
+            assert sorted(order) == sorted(held[b]) and k8[b, :m, 0].tolist() == order and ks[b, :m].tolist() == order
+            assert torch.equal(kv[b, :m].double(), torch.stack([held[b][s][0] for s in order]))
+            ref = torch.stack([held[b][s][1] for s in order])
+            assert bool(((acc[b, :m].double() - ref).abs() <= 1e-3 * ref + 1e-6).all())
+    assert dsa.dsa_get_device_status() == 0
