@@ -7,7 +7,6 @@ the library's CUDA kernels; there is no fallback path. Names follow the C entry 
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -525,40 +524,60 @@ def dsa_mla_out_absorb(o, w_uv, out=None, stream=None):
     return out
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Makes `device` current and yields the stream to launch on (its current one by default). What is
-    allocated inside belongs to that stream, so it is not handed out again before its work is done."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield _stream(torch.cuda.current_stream())
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
-            if stream.device != device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-            with torch.cuda.stream(stream):
-                yield _stream(stream)
+def _launch(device, stream, call):
+    """call(raw stream) with `device` current, on `stream` or its current one. What is allocated inside belongs
+    to that stream, so it is not handed out again before its work is done."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(device):
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
 
 
-def _one_device(first, **tensors):
-    for n, t in tensors.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{n} is on {t.device}, not on {first.device}: all tensors must be on one device")
-
-
-def _shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+def _arg(t, name, dtype, shape, device):
+    """Address of a contiguous `dtype` tensor of `shape` on `device`, a CUDA device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}: all tensors must be on one device")
+    return t.data_ptr()
+
+
+def _maybe(t, name, dtype, shape, device):
+    return None if t is None else _arg(t, name, dtype, shape, device)
+
+
+def _dims(t, name, dtype, n):
+    """The shape of a `dtype` tensor of n dimensions (its other properties are left to _arg)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions, got {list(t.shape)}")
+    return t.shape
 
 
 def _scratch(workspace, size, device):
     """The caller's workspace as (tensor, bytes), or a fresh one of `size` bytes."""
     if workspace is None:
         workspace = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
-    _need(workspace, workspace.dtype, "workspace")
-    if workspace.device != device:
-        raise ValueError("workspace must be on the tensors' device")
+    elif not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be contiguous and on {device}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -574,6 +593,9 @@ def dsa_rope_freqs(pairs: int, theta: float = 10000.0, factor: float = 1.0, orig
     return out
 
 
+_ROPE_DTYPES = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16, torch.float16: DSA_F16}
+
+
 def dsa_rope(x, pos, freqs, offset: int = 0, interleaved: bool = False, inverse: bool = False, scale: float = 1.0,
              out=None, stream=None):
     """x fp32, bf16 or fp16 [rows, heads, dim] or [rows, dim], features contiguous, rows and heads at any stride;
@@ -581,55 +603,54 @@ def dsa_rope(x, pos, freqs, offset: int = 0, interleaved: bool = False, inverse:
     [offset, offset + 2 pairs) of each head as pairs (2i, 2i+1) if interleaved, else (i, i + pairs), and copies the
     others into `out` (new and contiguous by default; out=x rotates in place). inverse=True with the same scale is the
     gradient with respect to x."""
-    dtypes = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16, torch.float16: DSA_F16}
-    if not isinstance(x, torch.Tensor) or x.dtype not in dtypes:
+    if not isinstance(x, torch.Tensor) or x.dtype not in _ROPE_DTYPES:
         raise TypeError("x must be a float32, bfloat16 or float16 tensor")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if x.dim() not in (2, 3):
-        raise ValueError(f"x must be [rows, heads, dim] or [rows, dim], got {list(x.shape)}")
-    _need(pos, torch.int32, "pos")
-    _need(freqs, torch.int64, "freqs")
-    rows, dim, pairs = x.shape[0], x.shape[-1], freqs.numel()
-    heads = x.shape[1] if x.dim() == 3 else 1
-    _shape(pos, (rows,), "pos")
+    shape = x.shape
+    if len(shape) not in (2, 3):
+        raise ValueError(f"x must be [rows, heads, dim] or [rows, dim], got {list(shape)}")
+    rows, dim = shape[0], shape[-1]
+    heads = shape[1] if len(shape) == 3 else 1
+    (pairs,) = _dims(freqs, "freqs", torch.int64, 1)
     if pairs < 1 or offset < 0 or offset + 2 * pairs > dim:
         raise ValueError(f"features [{offset}, {offset + 2 * pairs}) do not lie in a head of {dim}")
+    device = x.device
+    pos_ptr = _arg(pos, "pos", torch.int32, (rows,), device)
+    freqs_ptr = _arg(freqs, "freqs", torch.int64, (pairs,), device)
     if out is not None:
-        if not isinstance(out, torch.Tensor) or out.dtype != x.dtype:
+        if not isinstance(out, torch.Tensor) or out.dtype is not x.dtype:
             raise TypeError(f"out must be a {x.dtype} tensor")
-        _shape(out, x.shape, "out")
-    _one_device(x, pos=pos, freqs=freqs, out=out)
-    with _on(x.device, stream) as s:
-        if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        for t, n in ((x, "x"), (out, "out")):
-            if dim > 1 and t.stride(-1) != 1:
-                raise ValueError(f"the features of {n} must be contiguous")
+        if out.shape != shape or out.device != device:
+            raise ValueError(f"out must be {list(shape)} on {device}, got {list(out.shape)} on {out.device}")
+
+    def strides(t, name):
+        st = t.stride()
+        if dim > 1 and st[-1] != 1:
+            raise ValueError(f"the features of {name} must be contiguous")
+        return st[0] if rows > 1 else heads * dim, st[1] if len(shape) == 3 and heads > 1 else dim
+
+    def call(s):
+        y = torch.empty(shape, dtype=x.dtype, device=device) if out is None else out
         if rows == 0 or heads == 0:
-            return out
-        strides = [(t.stride(0) if rows > 1 else heads * dim, t.stride(1) if t.dim() == 3 and heads > 1 else dim)
-                   for t in (x, out)]
-        if out.data_ptr() != x.data_ptr() or strides[0] != strides[1]:
-            spans = [(t.data_ptr(), t.data_ptr() + t.element_size() * ((rows - 1) * r + (heads - 1) * h + dim))
-                     for t, (r, h) in zip((x, out), strides)]
-            if spans[0][0] < spans[1][1] and spans[1][0] < spans[0][1] and not _interleave(x, out, strides, heads, dim):
-                raise ValueError("out must be x itself or not overlap it")
+            return y
+        (xr, xh), (yr, yh) = strides(x, "x"), strides(y, "out")
+        xp, yp = x.data_ptr(), y.data_ptr()
+        if out is not None and (xp != yp or xr != yr or xh != yh):
+            size = x.element_size()
+            x_end, y_end = (xp + size * ((rows - 1) * xr + (heads - 1) * xh + dim),
+                            yp + size * ((rows - 1) * yr + (heads - 1) * yh + dim))
+            if xp < y_end and yp < x_end:
+                # the memory they span meets: they may still be different columns of the same rows
+                gap = (yp - xp) // size % xr if xr == yr and xr > 0 else 0
+                if gap < (heads - 1) * xh + dim or gap + (heads - 1) * yh + dim > xr:
+                    raise ValueError("out must be x itself or not overlap it")
         flags = (DSA_ROPE_INTERLEAVED if interleaved else 0) | (DSA_ROPE_INVERSE if inverse else 0)
-        rc = _lib.dsa_rope(_ptr(x), dtypes[x.dtype], rows, heads, strides[0][0], strides[0][1], dim, int(offset), pairs,
-                           _ptr(pos), _ptr(freqs), float(scale), flags, _ptr(out), strides[1][0], strides[1][1], s)
-    _check(rc, "dsa_rope")
-    return out
+        _check(_lib.dsa_rope(xp, _ROPE_DTYPES[x.dtype], rows, heads, xr, xh, dim, offset, pairs, pos_ptr, freqs_ptr, scale,
+                             flags, yp, yr, yh, s), "dsa_rope")
+        return y
 
-
-def _interleave(x, out, strides, heads, dim):
-    """Whether two tensors whose memory spans meet are disjoint columns of rows of one stride."""
-    (xr, xh), (outr, outh) = strides
-    if xr != outr:
-        return False
-    gap = (out.data_ptr() - x.data_ptr()) // x.element_size() % xr if xr else 0
-    width_x, width_out = (heads - 1) * xh + dim, (heads - 1) * outh + dim
-    return gap >= width_x and gap + width_out <= xr
+    return _launch(device, stream, call)
 
 
 def dsa_mla_shared_workspace_size(B: int, T: int, P: int, S_max: int) -> int:
@@ -643,69 +664,68 @@ def dsa_mla_shared(q, prefix, kv=None, q_pos=None, kv_len=None, softmax_scale: f
     [B,T,128,576], prefix bf16 [P,576] (or None), kv bf16 [B,S,576] with q_pos i32 [B,T] and kv_len i32 [B] (or all
     None): query (b, t) sees the prefix and the own rows s <= q_pos[b,t], s < kv_len[b] -> (out bf16 [B,T,128,512],
     lse fp32 [B,T,128])."""
-    _need(q, torch.bfloat16, "q")
-    if q.dim() != 4 or tuple(q.shape[2:]) != (128, 576):
-        raise ValueError(f"q must be [B, T, 128, 576], got {list(q.shape)}")
-    B, T = q.shape[:2]
+    B, T = _dims(q, "q", torch.bfloat16, 4)[:2]
+    device = q.device
+    q_ptr = _arg(q, "q", torch.bfloat16, (B, T, 128, 576), device)
     P = S = 0
+    p_ptr = kv_ptr = pos_ptr = len_ptr = None
     if prefix is not None:
-        _need(prefix, torch.bfloat16, "prefix")
-        P = prefix.shape[0]
-        _shape(prefix, (P, 576), "prefix")
+        P = _dims(prefix, "prefix", torch.bfloat16, 2)[0]
+        p_ptr = _arg(prefix, "prefix", torch.bfloat16, (P, 576), device)
     if kv is not None:
-        _need(kv, torch.bfloat16, "kv")
-        if kv.dim() != 3:
-            raise ValueError(f"kv must be [B, S_max, 576], got {list(kv.shape)}")
-        S = kv.shape[1]
-        _shape(kv, (B, S, 576), "kv")
-        for t, n, shape in ((q_pos, "q_pos", (B, T)), (kv_len, "kv_len", (B,))):
-            _need(t, torch.int32, n)
-            _shape(t, shape, n)
+        S = _dims(kv, "kv", torch.bfloat16, 3)[1]
+        kv_ptr = _arg(kv, "kv", torch.bfloat16, (B, S, 576), device)
+        pos_ptr = _arg(q_pos, "q_pos", torch.int32, (B, T), device)
+        len_ptr = _arg(kv_len, "kv_len", torch.int32, (B,), device)
     elif q_pos is not None or kv_len is not None:
         raise ValueError("q_pos and kv_len count own rows: they need kv")
-    for t, n, dt, shape in ((out, "out", torch.bfloat16, (B, T, 128, 512)), (lse, "lse", torch.float32, (B, T, 128))):
-        if t is not None:
-            _need(t, dt, n)
-            _shape(t, shape, n)
-    _one_device(q, prefix=prefix, kv=kv, q_pos=q_pos, kv_len=kv_len, out=out, lse=lse)
-    with _on(q.device, stream) as s:
-        if out is None:
-            out = torch.empty((B, T, 128, 512), dtype=torch.bfloat16, device=q.device)
-        if lse is None and want_lse:
-            lse = torch.empty((B, T, 128), dtype=torch.float32, device=q.device)
-        workspace, ws_len = _scratch(workspace, dsa_mla_shared_workspace_size(B, T, P, S), q.device)
-        rc = _lib.dsa_mla_shared(_ptr(q), _ptr(prefix), P, _ptr(kv), _ptr(q_pos), _ptr(kv_len), B, T, S,
-                                 float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), ws_len, s)
-    _check(rc, "dsa_mla_shared")
-    return out, lse
+    _maybe(out, "out", torch.bfloat16, (B, T, 128, 512), device)
+    _maybe(lse, "lse", torch.float32, (B, T, 128), device)
+
+    def call(s):
+        o = torch.empty((B, T, 128, 512), dtype=torch.bfloat16, device=device) if out is None else out
+        ls = torch.empty((B, T, 128), dtype=torch.float32, device=device) if lse is None and want_lse else lse
+        ws, size = _scratch(workspace, _lib.dsa_mla_shared_workspace_size(B, T, P, S), device)
+        _check(_lib.dsa_mla_shared(q_ptr, p_ptr, P, kv_ptr, pos_ptr, len_ptr, B, T, S, softmax_scale, o.data_ptr(),
+                                   None if ls is None else ls.data_ptr(), ws.data_ptr(), size, s), "dsa_mla_shared")
+        return o, ls
+
+    return _launch(device, stream, call)
 
 
-def _weights_args(q, kv, lse, acc, acc_out, w, width, others):
-    """Shape checks common to the two weight calls -> (B, T, S, acc_out)."""
-    _need(q, torch.bfloat16, "q")
-    if q.dim() != 4 or tuple(q.shape[2:]) != (128, 576):
-        raise ValueError(f"q must be [B, T, 128, 576], got {list(q.shape)}")
-    _need(kv, torch.bfloat16, "kv")
-    if kv.dim() != 3:
-        raise ValueError(f"kv must be [B, S_max, 576], got {list(kv.shape)}")
-    (B, T), S = q.shape[:2], kv.shape[1]
-    _shape(kv, (B, S, 576), "kv")
-    _need(lse, torch.float32, "lse")
-    _shape(lse, (B, T, 128), "lse")
+def _weights(name, q, kv, lse, own, width, softmax_scale, acc, acc_out, w, stream):
+    """The two weight calls: `own` are the addresses of what tells the rows, given B, T, S and the device."""
+    B, T = _dims(q, "q", torch.bfloat16, 4)[:2]
+    S = _dims(kv, "kv", torch.bfloat16, 3)[1]
+    device = q.device
+    q_ptr = _arg(q, "q", torch.bfloat16, (B, T, 128, 576), device)
+    kv_ptr = _arg(kv, "kv", torch.bfloat16, (B, S, 576), device)
+    lse_ptr = _arg(lse, "lse", torch.float32, (B, T, 128), device)
     if acc is None and acc_out is not None:
         raise ValueError("acc_out needs acc")
     acc_out = acc if acc_out is None else acc_out
-    for t, n in ((acc, "acc"), (acc_out, "acc_out")):
-        if t is not None:
-            _need(t, torch.float32, n)
-            _shape(t, (B, S), n)
+    acc_ptr = _maybe(acc, "acc", torch.float32, (B, S), device)
+    acc_out_ptr = _maybe(acc_out, "acc_out", torch.float32, (B, S), device)
     width = S if width is None else width
     if w is not None:
-        _need(w, torch.float32, "w")
-        if w.dim() != 3 or tuple(w.shape[:2]) != (B, T) or w.shape[2] < width or w.shape[2] % 4:
+        ld = _dims(w, "w", torch.float32, 3)[2]
+        if ld < width or ld % 4:
             raise ValueError(f"w must be [{B}, {T}, ld], ld >= {width} and a multiple of 4, got {list(w.shape)}")
-    _one_device(q, kv=kv, lse=lse, acc=acc, acc_out=acc_out, w=w, **others)
-    return B, T, S, acc_out
+        _arg(w, "w", torch.float32, (B, T, ld), device)
+    rows = own(B, T, device)
+
+    def call(s):
+        v = torch.empty((B, T, (width + 3) // 4 * 4), dtype=torch.float32, device=device) if w is None else w
+        if name == "dsa_mla_weights":
+            rc = _lib.dsa_mla_weights(q_ptr, kv_ptr, lse_ptr, *rows, B, T, S, softmax_scale, v.data_ptr(), v.shape[2],
+                                      acc_ptr, acc_out_ptr, s)
+        else:
+            rc = _lib.dsa_mla_weights_selected(q_ptr, kv_ptr, *rows, lse_ptr, B, T, S, width, softmax_scale, v.data_ptr(),
+                                               v.shape[2], acc_ptr, acc_out_ptr, s)
+        _check(rc, name)
+        return v, acc_out
+
+    return _launch(device, stream, call)
 
 
 def dsa_mla_weights(q, kv, lse, q_pos, kv_len, softmax_scale: float = MLA_SOFTMAX_SCALE, acc=None, acc_out=None, w=None,
@@ -714,36 +734,22 @@ def dsa_mla_weights(q, kv, lse, q_pos, kv_len, softmax_scale: float = MLA_SOFTMA
     fp32 [B,T,128] from the attention, q_pos i32 [B,T], kv_len i32 [B] -> (w fp32 [B,T,ld], acc). w is 0 at rows a
     query does not see; ld is S rounded up to 4. acc fp32 [B,S] grows by the queries' weights, in place unless acc_out
     is given (None: not wanted)."""
-    B, T, S, acc_out = _weights_args(q, kv, lse, acc, acc_out, w, None, dict(q_pos=q_pos, kv_len=kv_len))
-    for t, n, shape in ((q_pos, "q_pos", (B, T)), (kv_len, "kv_len", (B,))):
-        _need(t, torch.int32, n)
-        _shape(t, shape, n)
-    with _on(q.device, stream) as s:
-        if w is None:
-            w = torch.empty((B, T, (S + 3) // 4 * 4), dtype=torch.float32, device=q.device)
-        rc = _lib.dsa_mla_weights(_ptr(q), _ptr(kv), _ptr(lse), _ptr(q_pos), _ptr(kv_len), B, T, S, float(softmax_scale),
-                                  _ptr(w), w.shape[2], _ptr(acc), _ptr(acc_out), s)
-    _check(rc, "dsa_mla_weights")
-    return w, acc_out
+    def own(B, T, device):
+        return (_arg(q_pos, "q_pos", torch.int32, (B, T), device), _arg(kv_len, "kv_len", torch.int32, (B,), device))
+
+    return _weights("dsa_mla_weights", q, kv, lse, own, None, softmax_scale, acc, acc_out, w, stream)
 
 
 def dsa_mla_weights_selected(q, kv, idx, lse, softmax_scale: float = MLA_SOFTMAX_SCALE, acc=None, acc_out=None, w=None,
                              stream=None):
     """dsa_mla_weights for sparse attention: idx i32 [B,T,k] as given to dsa_sparse_mla (-1: unused slot), lse as it
     returned it -> (w fp32 [B,T,ld], acc); w[..., u] is the weight of slot u, ld is k rounded up to 4."""
-    _need(idx, torch.int32, "idx")
-    if idx.dim() != 3:
-        raise ValueError(f"idx must be [B, T, k], got {list(idx.shape)}")
-    k = idx.shape[2]
-    B, T, S, acc_out = _weights_args(q, kv, lse, acc, acc_out, w, k, dict(idx=idx))
-    _shape(idx, (B, T, k), "idx")
-    with _on(q.device, stream) as s:
-        if w is None:
-            w = torch.empty((B, T, (k + 3) // 4 * 4), dtype=torch.float32, device=q.device)
-        rc = _lib.dsa_mla_weights_selected(_ptr(q), _ptr(kv), _ptr(idx), _ptr(lse), B, T, S, k, float(softmax_scale),
-                                           _ptr(w), w.shape[2], _ptr(acc), _ptr(acc_out), s)
-    _check(rc, "dsa_mla_weights_selected")
-    return w, acc_out
+    k = _dims(idx, "idx", torch.int32, 3)[2]
+
+    def own(B, T, device):
+        return (_arg(idx, "idx", torch.int32, (B, T, k), device),)
+
+    return _weights("dsa_mla_weights_selected", q, kv, lse, own, k, softmax_scale, acc, acc_out, w, stream)
 
 
 def dsa_cache_evict_workspace_size(B: int, S_max: int, keep: int) -> int:
@@ -757,37 +763,34 @@ def dsa_cache_evict(acc, pos, kv_len, keep: int, recent: int = 0, sinks: int = 0
     the caches given (kv bf16 [B,S,576], k8 u8 [B,S,128] with k_scale fp32 [B,S]); acc, pos and kv_len are updated in
     place unless acc_out, pos_out, kv_len_out are given. Returns (acc, pos, kv_len, src), src i32 [B,keep] naming the
     row that each kept row came from (-1 behind them)."""
-    _need(acc, torch.float32, "acc")
-    if acc.dim() != 2:
-        raise ValueError(f"acc must be [B, S_max], got {list(acc.shape)}")
-    B, S = acc.shape
+    B, S = _dims(acc, "acc", torch.float32, 2)
     keep = int(keep)
     if keep < 1:
         raise ValueError("keep must be at least 1")
     if (k8 is None) != (k_scale is None):
         raise ValueError("k8 and k_scale go together")
-    acc_out = acc if acc_out is None else acc_out
-    pos_out = pos if pos_out is None else pos_out
-    kv_len_out = kv_len if kv_len_out is None else kv_len_out
-    for t, n, dt, shape in ((pos, "pos", torch.int32, (B, S)), (kv_len, "kv_len", torch.int32, (B,)),
-                            (acc_out, "acc_out", torch.float32, (B, S)), (pos_out, "pos_out", torch.int32, (B, S)),
-                            (kv_len_out, "kv_len_out", torch.int32, (B,)), (kv, "kv", torch.bfloat16, (B, S, 576)),
-                            (k8, "k8", torch.uint8, (B, S, 128)), (k_scale, "k_scale", torch.float32, (B, S)),
-                            (src, "src", torch.int32, (B, keep))):
-        if t is not None or n in ("pos", "kv_len"):
-            _need(t, dt, n)
-            _shape(t, shape, n)
-    _one_device(acc, pos=pos, kv_len=kv_len, acc_out=acc_out, pos_out=pos_out, kv_len_out=kv_len_out, kv=kv, k8=k8,
-                k_scale=k_scale, src=src)
-    with _on(acc.device, stream) as s:
-        if src is None:
-            src = torch.empty((B, keep), dtype=torch.int32, device=acc.device)
-        workspace, ws_len = _scratch(workspace, dsa_cache_evict_workspace_size(B, S, keep), acc.device)
-        rc = _lib.dsa_cache_evict(_ptr(acc), _ptr(pos), _ptr(kv_len), B, S, keep, int(recent), int(sinks), _ptr(kv),
-                                  _ptr(k8), _ptr(k_scale), _ptr(acc_out), _ptr(pos_out), _ptr(kv_len_out), _ptr(src),
-                                  _ptr(workspace), ws_len, s)
-    _check(rc, "dsa_cache_evict")
-    return acc_out, pos_out, kv_len_out, src
+    device = acc.device
+    acc_ptr = _arg(acc, "acc", torch.float32, (B, S), device)
+    pos_ptr = _arg(pos, "pos", torch.int32, (B, S), device)
+    len_ptr = _arg(kv_len, "kv_len", torch.int32, (B,), device)
+    kv_ptr = _maybe(kv, "kv", torch.bfloat16, (B, S, 576), device)
+    k8_ptr = _maybe(k8, "k8", torch.uint8, (B, S, 128), device)
+    ks_ptr = _maybe(k_scale, "k_scale", torch.float32, (B, S), device)
+    acc_out_ptr = acc_ptr if acc_out is None else _arg(acc_out, "acc_out", torch.float32, (B, S), device)
+    pos_out_ptr = pos_ptr if pos_out is None else _arg(pos_out, "pos_out", torch.int32, (B, S), device)
+    len_out_ptr = len_ptr if kv_len_out is None else _arg(kv_len_out, "kv_len_out", torch.int32, (B,), device)
+    _maybe(src, "src", torch.int32, (B, keep), device)
+
+    def call(s):
+        to = torch.empty((B, keep), dtype=torch.int32, device=device) if src is None else src
+        ws, size = _scratch(workspace, _lib.dsa_cache_evict_workspace_size(B, S, keep), device)
+        _check(_lib.dsa_cache_evict(acc_ptr, pos_ptr, len_ptr, B, S, keep, int(recent), int(sinks), kv_ptr, k8_ptr, ks_ptr,
+                                    acc_out_ptr, pos_out_ptr, len_out_ptr, to.data_ptr(), ws.data_ptr(), size, s),
+               "dsa_cache_evict")
+        return (acc if acc_out is None else acc_out, pos if pos_out is None else pos_out,
+                kv_len if kv_len_out is None else kv_len_out, to)
+
+    return _launch(device, stream, call)
 
 
 def dsa_sparse_mla_noalloc_scratch_bytes() -> int:
