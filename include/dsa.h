@@ -432,7 +432,7 @@ DSA_API size_t dsa_mla_shared_workspace_size(int B, int T, int P, int S_max);
  *           exp(softmax_scale * q . kv[b][s] - lse) for visible rows, 0 for the others up to S_max
  *           (entries from S_max to ld are left as they were)
  *   acc, acc_out  fp32 [B][S_max], or both NULL: acc_out[b][s] = acc[b][s] + sum over t of w[b][t][s],
- *           added in the order of t (the same bits every time); acc_out may be acc
+ *           added in a fixed order (the same bits every time); acc_out may be acc
  * Rows that a query does not see may hold anything. B, T, S_max >= 1; B <= 65535; B * T <= 2^23;
  * S_max at most DSA_MAX_POS; pointers 16-byte aligned.
  */

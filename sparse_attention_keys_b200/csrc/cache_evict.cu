@@ -78,6 +78,11 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int b = blockIdx.x / p.C;
+  // a barrier of the sequence's CTAs (a single one needs no cluster barrier)
+  auto sync_all = [&]() {
+    if (p.C == 1) __syncthreads();
+    else cluster_sync();
+  };
   grid_dep_wait();
   grid_dep_launch();
   const int n = max(0, min(__ldg(p.kv_len + b), p.S_max));
@@ -129,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     for (int d = 16; d; d >>= 1) newest = max(newest, __shfl_xor_sync(0xffffffffu, newest, d));
     if (lane == 0) cnt_sm[0] = (uint32_t)newest;
   }
-  cluster_sync();
+  sync_all();
   newest = INT32_MIN;
   for (int c = 0; c < p.C; ++c) newest = max(newest, (int)ld_cluster(&cnt_sm[0], (uint32_t)c));
   const int64_t recent_from = (int64_t)newest - p.recent;     // positions above it are protected
@@ -140,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
 
   // first digit, for both classes
   for (int r = r0 + tid; r < r1; r += kThreads) atomicAdd(&hist[is_safe(r) ? 1 : 0][weight(r) >> 21], 1u);
-  cluster_sync();
+  sync_all();
   // cluster-wide histogram of one class, two bins per thread, and its total
   auto merged = [&](int cls, uint32_t& h0, uint32_t& h1) {
     h0 = h1 = 0;
@@ -204,14 +209,14 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   for (int digit = 1; digit <= 2; ++digit) {
     const int shift = digit == 1 ? 10 : 0;
     const uint32_t mask = digit == 1 ? 0xffe00000u : 0xfffffc00u;
-    cluster_sync();                                            // every CTA has read the histograms
+    sync_all();                                            // every CTA has read the histograms
     hist[0][2 * tid] = hist[0][2 * tid + 1] = 0;
     __syncthreads();
     for (int r = r0 + tid; r < r1; r += kThreads) {
       const uint32_t k = weight(r);
       if ((k & mask) == prefix && is_safe(r) == (cls != 0)) atomicAdd(&hist[0][(k >> shift) & (digit == 1 ? 2047u : 1023u)], 1u);
     }
-    cluster_sync();
+    sync_all();
     find_bin(0, want, bin, above);
     prefix |= bin << shift;
     want -= above;
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     uint32_t total;
     const uint32_t base = block_scan(lane == 0 ? mine : 0u, total);
     if (tid == 0) cnt_sm[slot] = total;
-    cluster_sync();
+    sync_all();
     uint32_t before = 0;
     for (uint32_t c = 0; c < rank; ++c) before += ld_cluster(&cnt_sm[slot], c);
     return before + __shfl_sync(0xffffffffu, base, 0);
@@ -276,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     for (int c = 0; c < p.C; ++c) total += ld_cluster(&cnt_sm[2], (uint32_t)c);
     moves[0] = (int)total;
   }
-  cluster_sync();                                              // no CTA leaves while another reads it
+  sync_all();                                              // no CTA leaves while another reads it
 }
 
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p) {
@@ -341,9 +346,9 @@ int launch_cache_evict(const float* acc, const int32_t* pos, const int32_t* kv_l
   p.kv = reinterpret_cast<uint8_t*>(kv);
   p.k8 = k8;
   p.k_scale = k_scale;
-  // CTAs per sequence: enough that each takes at most 2048 rows, as far as one wave of SMs goes
+  // CTAs per sequence: enough that each takes at most 4096 rows, as far as one wave of SMs goes
   int C = 1;
-  while (C < kMaxCluster && (int64_t)C * 2048 < S_max && (int64_t)2 * C * B <= dsa_host::device_sm_count()) C *= 2;
+  while (C < kMaxCluster && (int64_t)C * 4096 < S_max && (int64_t)2 * C * B <= dsa_host::device_sm_count()) C *= 2;
   while (C < kMaxCluster && (int64_t)C * kCachedRows < S_max) C *= 2;
   p.C = C;
   const int64_t per_warp = (((int64_t)S_max + C * kWarps - 1) / (C * kWarps) + 31) / 32 * 32;

@@ -55,8 +55,7 @@ struct SharedParams {
   const uint16_t* kv;
   const int32_t* q_pos;
   const int32_t* kv_len;
-  int64_t BT;
-  int T, P, S_max;
+  int BT, T, P, S_max;
   float scale_log2;
   uint16_t* out;
   float* lse;
@@ -76,19 +75,18 @@ struct Unit {
   bool same, hasB;
 };
 
-__device__ __forceinline__ int visible(const SharedParams& p, int64_t tok, int b) {
+__device__ __forceinline__ int visible(const SharedParams& p, int tok, int b) {
   if (p.S_max == 0) return 0;
-  const int64_t v = (int64_t)__ldg(p.q_pos + tok) + 1;
-  const int64_t n = __ldg(p.kv_len + b);
-  return (int)max((int64_t)0, min(min(v, n), (int64_t)p.S_max));
+  const int last = __ldg(p.q_pos + tok), n = __ldg(p.kv_len + b);
+  return max(0, min(min(last, p.S_max - 1) + 1, n));
 }
 
-__device__ __forceinline__ Unit load_unit(const SharedParams& p, int64_t u) {
+__device__ __forceinline__ Unit load_unit(const SharedParams& p, int u) {
   Unit x;
-  const int64_t ta = 2 * u, tb = ta + 1;
+  const int ta = 2 * u, tb = ta + 1;
   x.hasB = tb < p.BT;
-  x.bA = (int)(ta / p.T);
-  x.bB = x.hasB ? (int)(tb / p.T) : x.bA;
+  x.bA = ta / p.T;
+  x.bB = x.hasB && tb == (x.bA + 1) * p.T ? x.bA + 1 : x.bA;
   x.same = x.bA == x.bB;
   x.visA = visible(p, ta, x.bA);
   x.visB = x.hasB ? visible(p, tb, x.bB) : 0;
@@ -133,10 +131,10 @@ __device__ __forceinline__ Tile get_tile(const SharedParams& p, const Unit& x, i
 // The pieces of a pair's range of tiles, one item after the other; every role walks it for itself.
 struct Walk {
   int64_t left;        // tiles left in the range
-  int64_t u;
+  int u;
   int half, t0, t1;    // the piece: tiles [t0, t1) of (u, half)
   Unit x;
-  __device__ __forceinline__ void start(const SharedParams& p, int64_t unit, int64_t off, int64_t count) {
+  __device__ __forceinline__ void start(const SharedParams& p, int unit, int64_t off, int64_t count) {
     left = count;
     u = unit;
     if (left <= 0) return;
@@ -180,8 +178,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* s_full = empty + kSlots;     // both [2]: scores ready
   uint64_t* p_full = s_full + 2;         // leader [2]: probabilities of both CTAs written
   uint64_t* pv_done = p_full + 2;        // both [2]: P V of the tile done
-  uint64_t* q_full = pv_done + 2;        // leader: Q of both CTAs landed
-  uint64_t* q_empty = q_full + 1;        // both: the piece's Q K^T done
+  uint64_t* q_full = pv_done + 2;        // leader [5]: two blocks of 64 features of both CTAs' Q landed
+  uint64_t* q_empty = q_full + 5;        // both: the piece's Q K^T done
   uint64_t* o_free = q_empty + 1;        // leader: both CTAs have read O
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
@@ -203,21 +201,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&p_full[i], 8);
       mbar_init(&pv_done[i], 1);
     }
-    mbar_init(q_full, 2);
+    for (int i = 0; i < 5; ++i) mbar_init(&q_full[i], 2);
     mbar_init(q_empty, 1);
     mbar_init(o_free, 8);
     fence_barrier_init();
   }
   if (warp == 2) pair_tmem_alloc(&tmem_base_sh, 512);
+  __syncwarp();
+  pair_arrive();                         // this thread's part of the set-up; waited for below
   grid_dep_wait();                       // lengths, queries and caches may come from the preceding kernel
   grid_dep_launch();
 
   // The pair's range of tiles: thread i sums the units [i * per, (i + 1) * per).
-  const int64_t units = (p.BT + 1) / 2;
-  const int64_t per = (units + kThreads - 1) / kThreads;
-  const int64_t ua = min(units, tid * per), ub = min(units, ua + per);
+  const int units = (p.BT + 1) / 2;
+  const int per = (units + kThreads - 1) / kThreads;
+  const int ua = min(units, tid * per), ub = min(units, ua + per);
   long long sum = 0;
-  for (int64_t u = ua; u < ub; ++u) sum += 2 * load_unit(p, u).tiles;
+  for (int u = ua; u < ub; ++u) sum += 2 * load_unit(p, u).tiles;
   long long pre = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -237,25 +237,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const long long excl = base + pre - sum;
   // no more pairs than tiles: the join walks over consecutive pairs, none of them without a tile
-  const long long active = min((long long)pairs, total);
-  const long long lo = pair < active ? total * pair / active : total;
-  const long long hi = pair < active ? total * (pair + 1) / active : total;
+  const int active = (int)min((long long)pairs, total);
+  const long long share = total < (1ll << 31) ? (long long)((uint32_t)total / (uint32_t)active) : total / active;
+  const int rest = (int)(total - share * active);
+  const long long lo = pair < active ? share * pair + min(pair, rest) : total;
+  const long long count = pair < active ? share + (pair < rest) : 0;
   if (sum > 0 && lo >= excl && lo < excl + sum) {
     long long off = lo - excl;
-    int64_t u = ua;
-    for (; u < ub; ++u) {
-      const long long n = 2 * load_unit(p, u).tiles;
-      if (off < n) break;
-      off -= n;
-    }
+    int u = ua;
+    if (per > 1)
+      for (; u < ub; ++u) {
+        const long long n = 2 * load_unit(p, u).tiles;
+        if (off < n) break;
+        off -= n;
+      }
     start_sh[0] = u;
     start_sh[1] = off;
   }
   __syncthreads();
-  pair_barrier();                        // barriers of both CTAs are initialised, both hold their TMEM
+  pair_wait();                           // barriers of both CTAs are initialised, both hold their TMEM
   const uint32_t tmem = tmem_base_sh;
   Walk w;
-  w.start(p, start_sh[0], start_sh[1], hi - lo);
+  w.start(p, (int)start_sh[0], start_sh[1], count);
 
   if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------------ loads
@@ -279,12 +282,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (++turn == 3) turn = 0;
     };
-    auto k_tile = [&](const Tile& t) {
+    auto k_tile = [&](const Tile& t, bool first) {
       for (int f = 0; ok && f < 9; f += 2, advance()) {
         if (turn != mine) continue;
         acquire();
         if (!ok) break;
         if (el) {
+          if (first) {                                   // with the first keys, the same features of Q
+            const uint32_t qbar = leader_addr(&q_full[f / 2]);
+            arrive_expect_tx_cluster(qbar, f < 8 ? 2 * kQBlock : kQBlock);
+            for (int i = f; i < min(f + 2, 9); ++i)
+              pair_load_2d(smem_u32(smem) + i * kQBlock, &q_map, qbar, 64 * i, (2 * w.u + (int)rank) * kHeads);
+          }
           const uint32_t bar = leader_addr(&full[slot]);
           arrive_expect_tx_cluster(bar, kSlot);          // there is no block 9: zeros
           load_slot(&p_map, &s_map, t.src, t.k0 + 64 * (int)rank, f, ring + slot * kSlot, bar);
@@ -335,23 +344,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     int piece = 0;
     for (; ok && w.valid(); w.next(p)) {
       if (get_tile(p, w.x, w.t0).most() == 0) continue;          // a unit without keys
-      if (mine == 0 && piece > 0) {
+      if (piece > 0) {
         if (!mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
       }
-      if (mine == 0 && el) {
-        const uint32_t bar = leader_addr(q_full);
-        arrive_expect_tx_cluster(bar, kQBytes);
-        for (int f = 0; f < 9; ++f)
-          pair_load_2d(smem_u32(smem) + f * kQBlock, &q_map, bar, 64 * f, (int32_t)((2 * w.u + rank) * kHeads));
-      }
       ++piece;
       Tile prev = get_tile(p, w.x, w.t0);
-      k_tile(prev);
+      k_tile(prev, true);
       for (int t = w.t0 + 1; ok && t < w.t1; ++t) {
         const Tile cur = get_tile(p, w.x, t);
-        k_tile(cur);
+        k_tile(cur, false);
         v_tile(prev, w.half);
         prev = cur;
       }
@@ -378,10 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
       };
-      auto qk = [&](uint32_t buf) {
+      auto qk = [&](uint32_t buf, bool first) {
         const uint32_t d = tmem + kTmemS + buf * kTile;
 #pragma unroll
         for (int f = 0; f < 9; f += 2) {
+          if (ok && first && !mbar_wait(&q_full[f / 2], piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q)) ok = false;
           if (ok) wait_full();
           if (!ok) break;
           const uint64_t a = q_desc + (uint64_t)((f * kQBlock) >> 4), b = k_desc + (uint64_t)((slot * kSlot) >> 4);
@@ -398,12 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok && w.valid(); w.next(p)) {
         Tile cur = get_tile(p, w.x, w.t0);
         if (cur.most() == 0) continue;
-        if (!mbar_wait(q_full, piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q)) break;
-        tc_fence_after();
         bool startedA = false, startedB = false;
-        qk(g & 1);
+        qk(g & 1, true);
         for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-          if (t + 1 < w.t1) qk((g + 1) & 1);
+          if (t + 1 < w.t1) qk((g + 1) & 1, false);
           else pair_commit(q_empty);
           if (!ok) break;
           cur = get_tile(p, w.x, t);
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int32_t info_cont = -1, info_head = -1;
     for (; ok && w.valid(); w.next(p)) {
-      const int64_t tok = 2 * w.u + rank;
+      const int tok = 2 * w.u + (int)rank;
       float m = -INFINITY, l = 0.f;
       bool any = false;
       for (int t = w.t0; ok && t < w.t1; ++t) {
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- the piece is done: output, or a partial for the join
       const bool whole = w.t0 == 0 && w.t1 == w.x.tiles;
       const int where = w.t0 == 0 ? 1 : 0;
-      if (!whole) (where ? info_head : info_cont) = (int32_t)(2 * w.u + w.half);
+      if (!whole) (where ? info_head : info_cont) = 2 * w.u + w.half;
       const bool had = get_tile(p, w.x, w.t0).most() > 0;
       if (had) {
         if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status,
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       if (whole) {
         if (tok < p.BT && w.half == 0 && p.lse)
-          p.lse[tok * kHeads + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+          p.lse[(int64_t)tok * kHeads + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       } else {
         *reinterpret_cast<float2*>(p.part_ml + (slot * 256 + prow) * 2) = make_float2(m, l);
       }
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (whole) {
           if (tok < p.BT) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * kHeads + row) * kDv + 256 * w.half + 32 * c);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)tok * kHeads + row) * kDv + 256 * w.half + 32 * c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint4 v;
@@ -601,52 +603,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) pair_tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of items that were cut: block (p, y) takes 32 rows of the item whose first piece
-// is the last one of pair p; the pieces that follow are the first ones of the next pairs.
+// Joins the pieces of items that were cut: block (p, y) takes 32 rows x 64 features of the item whose
+// first piece is the last one of pair p; the pieces that follow are the first ones of the next pairs.
 __global__ void __launch_bounds__(256) mla_shared_join_kernel(const SharedParams p, int pairs) {
+  extern __shared__ float2 ml_sh[];      // [pieces][32 rows]: maximum, sum
   const int pair = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  const int item = p.info[2 * pair + 1];
+  const int item = __ldcg(p.info + 2 * pair + 1);
   if (item < 0) return;
-  const int row = blockIdx.y * 32 + lane;
-  const int64_t tok = 2 * (int64_t)(item >> 1) + (row >> 7);
+  const int row = (blockIdx.y >> 2) * 32 + lane, col = (blockIdx.y & 3) * 64 + 8 * warp;
+  const int tok = 2 * (item >> 1) + (row >> 7);
   const int head = row & 127, half = item & 1;
-  if (tok >= p.BT) return;
-  int end = pair + 1;
-  while (end < pairs && p.info[2 * end] == item) ++end;
-  auto slot_of = [&](int q) { return q == pair ? (int64_t)pair * 2 + 1 : (int64_t)q * 2; };
-  float m = -INFINITY;
-  for (int q = pair; q < end; ++q) m = fmaxf(m, p.part_ml[(slot_of(q) * 256 + row) * 2]);
-  float l = 0.f;
-  float4 acc[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int q = pair; q < end; ++q) {
-    const int64_t slot = slot_of(q);
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot * 256 + row) * 2);
+  if (tok >= p.BT) return;               // the same for the whole block
+  int n = 1;                             // pieces
+  for (int q = pair + 1; q < pairs; q += 32) {
+    const uint32_t other = __ballot_sync(0xffffffffu, q + lane >= pairs || __ldcg(p.info + 2 * (q + lane)) != item);
+    n += other ? __ffs(other) - 1 : 32;
+    if (other) break;
+  }
+  auto slot_of = [&](int i) { return i == 0 ? (int64_t)pair * 2 + 1 : (int64_t)(pair + i) * 2; };
+  for (int i = warp; i < n; i += 8)
+    ml_sh[i * 32 + lane] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(i) * 256 + row);
+  __syncthreads();
+  float m = -INFINITY, l = 0.f;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, ml_sh[i * 32 + lane].x);
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  const float4* src = reinterpret_cast<const float4*>(p.part_o) + (int64_t)(col / 4) * 256 + row;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = ml_sh[i * 32 + lane];
     // a piece without a visible key has sum 0 and no maximum
     const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - m);
     l += ml.y * f;
-    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (slot * 64 + warp * 8) * 256 + row;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 v = src[i * 256];
-      acc[i].x = fmaf(v.x, f, acc[i].x);
-      acc[i].y = fmaf(v.y, f, acc[i].y);
-      acc[i].z = fmaf(v.z, f, acc[i].z);
-      acc[i].w = fmaf(v.w, f, acc[i].w);
+    for (int j = 0; j < 2; ++j) {
+      const float4 v = __ldcg(src + slot_of(i) * (64 * 256) + j * 256);
+      acc[j].x = fmaf(v.x, f, acc[j].x);
+      acc[j].y = fmaf(v.y, f, acc[j].y);
+      acc[j].z = fmaf(v.z, f, acc[j].z);
+      acc[j].w = fmaf(v.w, f, acc[j].w);
     }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint4* dst = reinterpret_cast<uint4*>(p.out + (tok * kHeads + head) * kDv + 256 * half + 32 * warp);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 a = acc[2 * i], b = acc[2 * i + 1];
-    dst[i] = make_uint4(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv), pack_bf16(b.x * inv, b.y * inv),
-                        pack_bf16(b.z * inv, b.w * inv));
-  }
-  if (warp == 0 && half == 0 && p.lse) p.lse[tok * kHeads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  const int64_t out_row = (int64_t)tok * kHeads + head;
+  *reinterpret_cast<uint4*>(p.out + out_row * kDv + 256 * half + col) =
+      make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
+                 pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
+  if (col == 0 && half == 0 && p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 namespace {
@@ -676,7 +680,7 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
   p.kv = kv;
   p.q_pos = q_pos;
   p.kv_len = kv_len;
-  p.BT = (int64_t)B * T;
+  p.BT = B * T;
   p.T = T;
   p.P = P;
   p.S_max = S_max;
@@ -718,7 +722,7 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
   }
   int rc = dsa_host::launch_pairs(mla_shared_kernel, (unsigned)pairs, kThreads, kSmem, stream, q_map, pm, sm, p);
   if (rc != DSA_OK) return rc;
-  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)pairs, 8), dim3(256), 0, stream, p, pairs);
+  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)pairs, 32), dim3(256), (size_t)pairs * 32 * 8, stream, p, pairs);
 }
 
 }  // namespace dsa

@@ -349,7 +349,23 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
             s4[3] += exp2_approx(fmaf(__uint_as_float(y[3]), p.scale_log2, -l4.w));
           }
         }
-        if (u < r.keys) p.w[r.tok * p.ld + u] = take ? (s4[0] + s4[1]) + (s4[2] + s4[3]) : 0.f;
+        if (u < r.keys) {
+          const float sum = take ? (s4[0] + s4[1]) + (s4[2] + s4[3]) : 0.f;
+          p.w[r.tok * p.ld + u] = sum;
+          if (!SELECTED && p.T == 1 && p.acc_out) p.acc_out[r.tok * p.S_max + u] = p.acc[r.tok * p.S_max + u] + sum;
+        }
+      }
+    }
+  }
+  if (!SELECTED && p.T == 1 && (warp == 2 || warp == 3)) {
+    // one query per sequence: its hidden rows get their zeros here, and acc is done above
+    const int64_t n = p.BT * p.S_max;
+    for (int64_t i = (int64_t)blockIdx.x * 64 + (warp - 2) * 32 + lane; i < n; i += (int64_t)gridDim.x * 64) {
+      const int64_t tok = i / p.S_max;
+      const int s = (int)(i - tok * p.S_max);
+      if (s >= keys_of(p, tok)) {
+        p.w[tok * p.ld + s] = 0.f;
+        if (p.acc_out) p.acc_out[i] = p.acc[i];
       }
     }
   }
@@ -359,20 +375,35 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
   if (warp == 2) tmem_dealloc(tmem, 512);
 }
 
-// Dense: zeros behind each query's keys, and acc_out = acc + the weights of the queries in their order.
+// Dense, several queries per sequence: zeros behind each query's keys, and acc_out = acc + the weights
+// of the queries. Each of 8 warps adds every eighth query for 32 rows, then the eight sums join in order.
 __global__ void __launch_bounds__(256) mla_weights_sum_kernel(const WeightsParams p) {
+  __shared__ float part[8][32];
   const int64_t b = blockIdx.y;
-  const int s = blockIdx.x * 256 + threadIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.x * 32 + lane;
   grid_dep_wait();
   grid_dep_launch();
-  if (s >= p.S_max) return;
-  float a = p.acc_out ? p.acc[b * p.S_max + s] : 0.f;
-  float* w = p.w + b * p.T * p.ld + s;
-  for (int t = 0; t < p.T; ++t) {
-    if (s < keys_of(p, b * p.T + t)) a += p.acc_out ? w[t * p.ld] : 0.f;
-    else w[t * p.ld] = 0.f;
+  const int len = min(__ldg(p.kv_len + b), p.S_max);
+  float a = 0.f;
+  if (s < p.S_max) {
+    const int32_t* last = p.q_pos + b * p.T;
+    float* w = p.w + b * p.T * p.ld + s;
+#pragma unroll 4
+    for (int t = warp; t < p.T; t += 8) {
+      if (s < len && s <= __ldg(last + t)) {
+        if (p.acc_out) a += w[t * p.ld];
+      } else {
+        w[t * p.ld] = 0.f;
+      }
+    }
   }
-  if (p.acc_out) p.acc_out[b * p.S_max + s] = a;
+  part[warp][lane] = a;
+  __syncthreads();
+  if (warp == 0 && s < p.S_max && p.acc_out) {
+    a = p.acc[b * p.S_max + s];
+    for (int i = 0; i < 8; ++i) a += part[i][lane];
+    p.acc_out[b * p.S_max + s] = a;
+  }
 }
 
 // Selected: acc_out = acc + the weights of the queries in their order; a block holds kRange positions of
@@ -426,8 +457,9 @@ int launch_weights(const uint16_t* q, const WeightsParams& p, int64_t B, cudaStr
   const int rc = dsa_host::launch(mla_weights_kernel<SELECTED>, dim3(grid), dim3(SELECTED ? 384 : 256), kSmem, stream, q_map,
                                   k_map, p);
   if (rc != DSA_OK) return rc;
+  if (!SELECTED && p.T == 1) return DSA_OK;
   if (!SELECTED)
-    return dsa_host::launch(mla_weights_sum_kernel, dim3((unsigned)((p.S_max + 255) / 256), (unsigned)B), dim3(256), 0, stream, p);
+    return dsa_host::launch(mla_weights_sum_kernel, dim3((unsigned)((p.S_max + 31) / 32), (unsigned)B), dim3(256), 0, stream, p);
   if (!p.acc_out) return DSA_OK;
   return dsa_host::launch(mla_weights_scatter_kernel, dim3((unsigned)((p.S_max + kRange - 1) / kRange), (unsigned)B),
                           dim3(1024), 0, stream, p);

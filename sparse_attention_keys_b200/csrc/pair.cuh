@@ -24,6 +24,11 @@ __device__ __forceinline__ void pair_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of pair_barrier: what a thread wrote before pair_arrive is seen by both CTAs after
+// every thread's pair_wait.
+__device__ __forceinline__ void pair_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void pair_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // One thread of a converged warp (the compiler then keeps the MMA operands in uniform registers).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

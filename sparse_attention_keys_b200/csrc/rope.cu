@@ -189,8 +189,11 @@ int launch_typed(RopeParams p, bool interleaved, bool in_place, cudaStream_t str
   p.rot_items = interleaved ? 2 * p.pairs / e : p.pairs / V;
   p.pass_items = in_place ? 0 : (p.dim - 2 * p.pairs) / V;
   p.unit_items = p.rot_items + p.pass_items;
-  // about 1024 items a block, and no more sines than its shared memory holds
-  const int most = std::max(1, std::min(kBatch * kThreads / p.unit_items, kMaxCs / p.pairs));
+  // 1024 items a block, down to one a thread where that leaves SMs without work, and no more sines
+  // than its shared memory holds (16384 keys of 64 features: 10.4 us with 1024 items, 0 with 256)
+  int64_t items = kBatch * kThreads;
+  while (items > kThreads && p.units * p.unit_items < items * 8 * dsa_host::device_sm_count()) items /= 2;
+  const int most = std::max(1, std::min((int)items / p.unit_items, kMaxCs / p.pairs));
   p.per_block = (int)std::min<int64_t>(most, p.units);
   p.div_items = small_div((uint32_t)p.unit_items);
   p.div_heads = small_div((uint32_t)p.heads);
