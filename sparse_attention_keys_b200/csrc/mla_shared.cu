@@ -5,21 +5,27 @@
 // out = softmax(z) . key[0:512], lse = ln sum e^z. The prefix is stored once and its tiles are
 // multiplied with the queries of every sequence, so its part is a matrix product with B*T*128 rows.
 //
-// Work. Two tokens (256 rows of q) form a unit; a CTA pair (cta_group::2, M = 256, one token per
-// CTA) accumulates one half (256 features) of the unit's output, since 128 x 512 fp32 would fill
-// the whole TMEM and leave none for the scores. So the scores are computed by both halves: 832
-// instead of 544 multiply-adds per (row, key, CTA pair), the price of keeping O in TMEM. A unit's
-// keys are the prefix, then the own rows of its token(s), in tiles of 128, all accumulated into one
-// O with a running maximum and sum. The tiles of all (unit, half) items in a row are cut into equal
-// ranges, one per CTA pair; an item that a cut divides leaves fp32 partials in the workspace, which
-// a second kernel joins. Every pair holds at most two such pieces, so the workspace is bounded
-// whatever the lengths are, and the device alone reads the lengths.
+// Work. Two tokens (256 rows of q) form a unit. Its keys are the prefix, then the own rows of its
+// token(s), in tiles of 128, all accumulated into one output with a running maximum and sum. A
+// 128 x 512 fp32 output fills a whole TMEM and leaves none for scores, so a unit runs on a cluster of
+// four CTAs, two tcgen05 pairs (M = 256, one token per CTA of a pair): the score pair (ranks 0, 1)
+// computes Q K^T and the softmax, the value pair (ranks 2, 3) holds the output and computes P V. Per
+// tile that is 36 MMAs of 256 x 128 x 16 (2306 cycles) against 16 of 256 x 256 x 16 (2052), side by
+// side: nothing is computed twice. (Before, two pairs held half of the output each and both computed
+// the scores: 3330 cycles per tile, and 1.53 times the arithmetic of this power-bound kernel.)
+// The probabilities go from the score CTA's shared memory into its value CTA's with bulk copies that
+// count on the receiver's barrier, with the factor by which the running maximum moved.
 //
-// Per CTA: Q (128 x 576, 144 KB) stays in shared memory; K and V stream through one ring of 16 KB
-// slots of 64 keys x 128 features in the order the MMAs consume them (K: this CTA's half of the
-// tile's keys, five slots; V: its half of the 256 output features, two slots). TMEM: O [0, 256),
-// two score buffers of 128 columns; the probabilities (bf16) replace the scores they came from and
-// are the A operand of P V. Q K^T of tile j + 1 runs while the softmax of tile j does.
+// The tiles of all units in a row are cut into equal ranges, one per cluster; a unit that a cut
+// divides leaves fp32 partials in the workspace, which a second kernel joins. Every cluster holds at
+// most two such pieces, so the workspace is bounded whatever the lengths are, and the device alone
+// reads the lengths.
+//
+// Score CTA: Q features 0..511 in TMEM [0, 256) (A operand, bf16 pairs), 512..575 in shared memory;
+// two score buffers in TMEM [256, 512); two staging buffers for P; K through a ring of 16 KB slots
+// (64 keys x 128 features, this CTA's half of the tile's keys, five slots a tile).
+// Value CTA: O in all 512 TMEM columns; two P buffers; V through a ring of the same slots (64 keys x
+// 128 features: this CTA's half of the 256 features of an MMA, four slots a tile).
 #include <math.h>
 
 #include <algorithm>
@@ -34,16 +40,19 @@ namespace {
 constexpr int kHeads = 128;
 constexpr int kDqk = 576, kDv = 512;
 constexpr int kTile = 128;                         // keys per tile
-constexpr int kQBlock = kHeads * 128;              // 16 KB: 64 features of 128 rows
-constexpr int kQBytes = 9 * kQBlock;
-constexpr int kSlot = 16384;                       // 64 keys x two blocks of 64 features
-constexpr int kSlots = 5;
-constexpr int kOffRing = kQBytes;
-constexpr int kOffBar = kOffRing + kSlots * kSlot;
+constexpr int kBlock = 16384;                      // 64 features (or keys) of 128 rows; a ring slot
+constexpr int kSlots = 8;
+// the same offsets in every CTA of the cluster, so that one descriptor serves both CTAs of a pair and
+// a buffer's address in another CTA is its own address there
+constexpr int kOffP = kBlock;                      // [2][2 blocks of 64 keys]: staging, or P
+constexpr int kOffRing = kOffP + 4 * kBlock;       // [0, kBlock): Q features 512..575
+constexpr int kOffAlpha = kOffRing + kSlots * kBlock;   // [2][128] fp32
+constexpr int kOffL = kOffAlpha + 2 * 128 * 4;     // [4][128] fp32
+constexpr int kOffBar = kOffL + 4 * 128 * 4;
 constexpr int kSmem = 1024 + kOffBar + 512;
-static_assert(kSmem <= 232448, "shared memory per CTA");
-constexpr int kThreads = 256;
-constexpr uint32_t kTmemS = 256;                   // O in [0, 256), scores in 2 x 128 columns
+static_assert(kSmem + 1024 <= 232448, "shared memory per CTA");
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemS = 256;                   // score CTA: Q in [0, 256), scores in 2 x 128 columns
 constexpr float kLn2 = 0.69314718055994530942f;
 // The running maximum moves, and O is rescaled, only when a tile exceeds it by 2^32: P stays below
 // 2^32, where bf16 has its full relative precision, and the sums stay far inside fp32.
@@ -52,6 +61,7 @@ constexpr float kRescale = 32.0f;
 }  // namespace
 
 struct SharedParams {
+  const uint16_t* q;
   const uint16_t* kv;
   const int32_t* q_pos;
   const int32_t* kv_len;
@@ -59,9 +69,9 @@ struct SharedParams {
   float scale_log2;
   uint16_t* out;
   float* lse;
-  int32_t* info;       // [pairs][2]: the item continued from the previous pair, the item cut at the end (-1: none)
-  float* part_ml;      // [pairs][2][256][2]: maximum (log2 units), sum
-  float* part_o;       // [pairs][2][64][256][4]: feature group, row, feature
+  int32_t* info;       // [clusters][2]: the unit continued from the previous cluster, the one cut at the end (-1: none)
+  float* part_ml;      // [clusters][2][256][2]: maximum (log2 units), sum
+  float* part_o;       // [clusters][2][128][256][4]: feature group, row, feature
   int* status;
 };
 
@@ -128,33 +138,29 @@ __device__ __forceinline__ Tile get_tile(const SharedParams& p, const Unit& x, i
   return r;
 }
 
-// The pieces of a pair's range of tiles, one item after the other; every role walks it for itself.
+// The pieces of a cluster's range of tiles, one unit after the other; every role walks it for itself.
 struct Walk {
   int64_t left;        // tiles left in the range
-  int u;
-  int half, t0, t1;    // the piece: tiles [t0, t1) of (u, half)
+  int u, t0, t1;       // the piece: tiles [t0, t1) of unit u
   Unit x;
   __device__ __forceinline__ void start(const SharedParams& p, int unit, int64_t off, int64_t count) {
     left = count;
     u = unit;
+    t0 = (int)off;
     if (left <= 0) return;
     x = load_unit(p, u);
-    half = off >= x.tiles;
-    t0 = (int)(off - (half ? x.tiles : 0));
     t1 = (int)min((int64_t)x.tiles, t0 + left);
   }
   __device__ __forceinline__ bool valid() const { return left > 0; }
   __device__ __forceinline__ void next(const SharedParams& p) {
     left -= t1 - t0;
     if (left <= 0) return;
-    if (half) {
-      ++u;
-      x = load_unit(p, u);
-    }
-    half ^= 1;
+    x = load_unit(p, ++u);
     t0 = 0;
     t1 = (int)min((int64_t)x.tiles, left);
   }
+  // a unit that sees no key has one empty tile: only its zeros are written
+  __device__ __forceinline__ bool empty(const SharedParams& p) const { return get_tile(p, x, t0).most() == 0; }
 };
 
 // Rows [row, row + 64) of a tile's source, feature blocks [block, block + 2) of 64: [block][row][64]
@@ -170,25 +176,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     mla_shared_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap p_map,
                       const __grid_constant__ CUtensorMap s_map, const SharedParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  // both CTAs of a pair see the same offsets: the MMA reads them with one descriptor
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  float* alpha_sm = reinterpret_cast<float*>(smem + kOffAlpha);
+  float* l_sm = reinterpret_cast<float*>(smem + kOffL);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint64_t* full = bars;                 // leader: both CTAs' parts of the slot have landed
-  uint64_t* empty = full + kSlots;       // both: the MMAs that read the slot are done
-  uint64_t* s_full = empty + kSlots;     // both [2]: scores ready
-  uint64_t* p_full = s_full + 2;         // leader [2]: probabilities of both CTAs written
-  uint64_t* pv_done = p_full + 2;        // both [2]: P V of the tile done
-  uint64_t* q_full = pv_done + 2;        // leader [5]: two blocks of 64 features of both CTAs' Q landed
-  uint64_t* q_empty = q_full + 5;        // both: the piece's Q K^T done
-  uint64_t* o_free = q_empty + 1;        // leader: both CTAs have read O
+  uint64_t* full = bars;                 // leader of each pair [kSlots]: both CTAs' parts of the slot have landed
+  uint64_t* empty = full + kSlots;       // both of a pair [kSlots]: the MMAs that read the slot are done
+  uint64_t* s_full = empty + kSlots;     // score CTAs [2]: scores ready
+  uint64_t* s_free = s_full + 2;         // rank 0 [2]: both score CTAs have read the scores
+  uint64_t* p_full = s_free + 2;         // value CTAs [2]: this CTA's probabilities and factors have landed
+  uint64_t* p_ready = p_full + 2;        // rank 2 [2]: both value CTAs have them, O is rescaled
+  uint64_t* pv_done = p_ready + 2;       // all [2]: P V of the tile done
+  uint64_t* l_full = pv_done + 2;        // value CTAs [4]: the piece's sums have landed
+  uint64_t* q_full = l_full + 4;         // rank 0: Q of both score CTAs in place
+  uint64_t* q_empty = q_full + 1;        // score CTAs: the piece's Q K^T done
+  uint64_t* o_free = q_empty + 1;        // rank 2: both value CTAs have read O
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ long long scan_sh[kThreads / 32];
-  __shared__ long long start_sh[2];      // first unit of this pair's range, offset in its 2 x tiles
+  __shared__ long long start_sh[2];      // first unit of this cluster's range, first tile of it
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = pair_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const uint32_t rank = cluster_rank(), side = rank & 1;     // side: the token of the unit, the half of a B operand
+  const bool values = rank >= 2;
+  const int cluster = blockIdx.x >> 2, clusters = gridDim.x >> 2;
 
   if (tid == 0) {
     abort_flag = 0;
@@ -198,26 +209,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 8);
+      mbar_init(&s_free[i], 8);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&p_ready[i], 16);
       mbar_init(&pv_done[i], 1);
     }
-    for (int i = 0; i < 5; ++i) mbar_init(&q_full[i], 2);
+    for (int i = 0; i < 4; ++i) mbar_init(&l_full[i], 4);
+    mbar_init(q_full, 8 + 2);
     mbar_init(q_empty, 1);
-    mbar_init(o_free, 8);
+    mbar_init(o_free, 16);
     fence_barrier_init();
   }
   if (warp == 2) pair_tmem_alloc(&tmem_base_sh, 512);
   __syncwarp();
-  pair_arrive();                         // this thread's part of the set-up; waited for below
+  cluster_arrive();                      // this thread's part of the set-up; waited for below
   grid_dep_wait();                       // lengths, queries and caches may come from the preceding kernel
   grid_dep_launch();
 
-  // The pair's range of tiles: thread i sums the units [i * per, (i + 1) * per).
+  // The cluster's range of tiles: thread i sums the units [i * per, (i + 1) * per).
   const int units = (p.BT + 1) / 2;
   const int per = (units + kThreads - 1) / kThreads;
   const int ua = min(units, tid * per), ub = min(units, ua + per);
   long long sum = 0;
-  for (int u = ua; u < ub; ++u) sum += 2 * load_unit(p, u).tiles;
+  for (int u = ua; u < ub; ++u) sum += load_unit(p, u).tiles;
   long long pre = sum;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -236,18 +250,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     total += scan_sh[w];
   }
   const long long excl = base + pre - sum;
-  // no more pairs than tiles: the join walks over consecutive pairs, none of them without a tile
-  const int active = (int)min((long long)pairs, total);
+  // no more clusters than tiles: the join walks over consecutive clusters, none of them without a tile
+  const int active = (int)min((long long)clusters, total);
   const long long share = total < (1ll << 31) ? (long long)((uint32_t)total / (uint32_t)active) : total / active;
   const int rest = (int)(total - share * active);
-  const long long lo = pair < active ? share * pair + min(pair, rest) : total;
-  const long long count = pair < active ? share + (pair < rest) : 0;
+  const long long lo = cluster < active ? share * cluster + min(cluster, rest) : total;
+  const long long count = cluster < active ? share + (cluster < rest) : 0;
   if (sum > 0 && lo >= excl && lo < excl + sum) {
     long long off = lo - excl;
     int u = ua;
     if (per > 1)
       for (; u < ub; ++u) {
-        const long long n = 2 * load_unit(p, u).tiles;
+        const int n = load_unit(p, u).tiles;
         if (off < n) break;
         off -= n;
       }
@@ -255,119 +269,113 @@ __global__ void __launch_bounds__(kThreads, 1)
     start_sh[1] = off;
   }
   __syncthreads();
-  pair_wait();                           // barriers of both CTAs are initialised, both hold their TMEM
+  cluster_wait();                        // the barriers of every CTA are initialised, every pair holds its TMEM
   const uint32_t tmem = tmem_base_sh;
+  const uint32_t ring = smem_u32(smem + kOffRing);
   Walk w;
   w.start(p, (int)start_sh[0], start_sh[1], count);
 
   if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------------ loads
-    // Waiting for a slot and issuing its load take one warp about 400 cycles, more than the MMAs of a
-    // block (260): three warps take the blocks in turn (shared_chunk 3059 -> 0 us).
+    // Waiting for a slot and issuing its load take a warp about as long as the MMAs that free it, so
+    // three warps take the slots in turn.
     const int mine = warp == 0 ? 0 : warp - 1;
-    int turn = 0;
+    int turn = 0, slot = 0, piece = 0;
+    uint32_t ph = 1;                     // a fresh slot counts as freed
     const bool el = elect_one();
-    const uint32_t ring = smem_u32(smem + kOffRing);
-    int slot = 0, round = 0;
     bool ok = true;
     auto acquire = [&]() {
-      if (round > 0 && !mbar_wait(&empty[slot], (round + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY))
-        ok = false;
+      if (!mbar_wait(&empty[slot], ph, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY)) ok = false;
       ok = __all_sync(0xffffffffu, ok);
     };
     auto advance = [&]() {
       if (++slot == kSlots) {
         slot = 0;
-        ++round;
+        ph ^= 1;
       }
       if (++turn == 3) turn = 0;
     };
-    auto k_tile = [&](const Tile& t, bool first) {
+    auto k_tile = [&](const Tile& t) {
       for (int f = 0; ok && f < 9; f += 2, advance()) {
         if (turn != mine) continue;
         acquire();
         if (!ok) break;
         if (el) {
-          if (first) {                                   // with the first keys, the same features of Q
-            const uint32_t qbar = leader_addr(&q_full[f / 2]);
-            arrive_expect_tx_cluster(qbar, f < 8 ? 2 * kQBlock : kQBlock);
-            for (int i = f; i < min(f + 2, 9); ++i)
-              pair_load_2d(smem_u32(smem) + i * kQBlock, &q_map, qbar, 64 * i, (2 * w.u + (int)rank) * kHeads);
-          }
-          const uint32_t bar = leader_addr(&full[slot]);
-          arrive_expect_tx_cluster(bar, kSlot);          // there is no block 9: zeros
-          load_slot(&p_map, &s_map, t.src, t.k0 + 64 * (int)rank, f, ring + slot * kSlot, bar);
+          const uint32_t bar = cluster_addr(&full[slot], 0);
+          arrive_expect_tx_cluster(bar, kBlock);         // there is no block 9: zeros
+          load_slot(&p_map, &s_map, t.src, t.k0 + 64 * (int)side, f, ring + slot * kBlock, bar);
         }
       }
     };
-    auto v_tile = [&](const Tile& t, int half) {
+    auto v_slot = [&](const Tile& t, int kb, int half) {
       const int n = t.most();
-      for (int kb = 0; ok && kb < n; kb += 64, advance()) {
-        if (turn != mine) continue;
-        acquire();
-        if (!ok) break;
-        const uint32_t dst = ring + slot * kSlot, bar = leader_addr(&full[slot]);
-        const int block = 4 * half + 2 * (int)rank;
-        if (t.src < 0 || n - kb >= 64) {
-          if (el) {
-            arrive_expect_tx_cluster(bar, kSlot);
-            load_slot(&p_map, &s_map, t.src, t.k0 + kb, block, dst, bar);
-          }
-        } else {
-          // the rows behind the last visible key may hold anything, and 0 * NaN is NaN: the warp
-          // copies the visible rows itself and puts zeros behind them
-          const uint16_t* src = p.kv + ((int64_t)t.src * p.S_max + t.k0 + kb) * kDqk + 64 * block;
+      const uint32_t dst = ring + slot * kBlock, bar = cluster_addr(&full[slot], 2);
+      const int block = 4 * half + 2 * (int)side;
+      if (t.src < 0 || n - kb >= 64) {
+        if (el) {
+          arrive_expect_tx_cluster(bar, kBlock);
+          load_slot(&p_map, &s_map, t.src, t.k0 + kb, block, dst, bar);
+        }
+        return;
+      }
+      // the rows behind the last visible key may hold anything, and 0 * NaN is NaN: the warp copies
+      // the visible rows itself and puts zeros behind them
+      const uint16_t* src = p.kv + ((int64_t)t.src * p.S_max + t.k0 + kb) * kDqk + 64 * block;
 #pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint4 v[16];
+      for (int h = 0; h < 2; ++h) {
+        uint4 v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = 32 * h + 2 * i + (lane >> 4), c = lane & 15;    // row, 16-byte chunk of its 256 bytes
-              v[i] = r < n - kb ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * kDqk) + c) : make_uint4(0, 0, 0, 0);
-            }
+        for (int i = 0; i < 16; ++i) {
+          const int r = 32 * h + 2 * i + (lane >> 4), c = lane & 15;    // row, 16-byte chunk of its 256 bytes
+          v[i] = r < n - kb ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * kDqk) + c) : make_uint4(0, 0, 0, 0);
+        }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = 32 * h + 2 * i + (lane >> 4), c = lane & 15;
-              const uint32_t a = dst + 8192 * (c >> 3) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[i].x), "r"(v[i].y), "r"(v[i].z),
-                           "r"(v[i].w)
-                           : "memory");
-            }
-          }
-          fence_proxy_async_smem();
-          cluster_fence();
-          __syncwarp();
-          if (el) arrive_cluster(bar);
+        for (int i = 0; i < 16; ++i) {
+          const int r = 32 * h + 2 * i + (lane >> 4), c = lane & 15;
+          st_shared_16(dst + 8192 * (c >> 3) + r * 128 + (((c & 7) ^ (r & 7)) << 4), v[i]);
         }
       }
+      fence_proxy_async_smem();
+      cluster_fence();
+      __syncwarp();
+      if (el) arrive_cluster(bar);
     };
-    int piece = 0;
     for (; ok && w.valid(); w.next(p)) {
-      if (get_tile(p, w.x, w.t0).most() == 0) continue;          // a unit without keys
-      if (piece > 0) {
-        if (!mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY)) ok = false;
+      if (w.empty(p)) continue;
+      if (!values && mine == 0) {
+        // the last 64 features of Q
+        if (piece > 0 && !mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        if (el) {
+          const uint32_t bar = cluster_addr(q_full, 0);
+          arrive_expect_tx_cluster(bar, kBlock);
+          pair_load_2d(smem_u32(smem), &q_map, bar, 512, (2 * w.u + (int)side) * kHeads);
+        }
       }
       ++piece;
-      Tile prev = get_tile(p, w.x, w.t0);
-      k_tile(prev, true);
-      for (int t = w.t0 + 1; ok && t < w.t1; ++t) {
-        const Tile cur = get_tile(p, w.x, t);
-        k_tile(cur, false);
-        v_tile(prev, w.half);
-        prev = cur;
+      for (int t = w.t0; ok && t < w.t1; ++t) {
+        const Tile tile = get_tile(p, w.x, t);
+        if (!values) {
+          k_tile(tile);
+          continue;
+        }
+        for (int i = 0; ok && 64 * (i >> 1) < tile.most(); ++i, advance()) {
+          if (turn != mine) continue;
+          acquire();
+          if (ok) v_slot(tile, 64 * (i >> 1), i & 1);
+        }
       }
-      if (ok) v_tile(prev, w.half);
+    }
+    // the last MMAs' arrivals have to reach this CTA before it leaves
+    if (mine == 0) {
+      for (int i = 0; ok && i < kSlots; ++i, advance()) acquire();
+      if (ok && !values && piece > 0)
+        mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issue: one thread of the leader
-    if (rank == 0 && elect_one()) {
-      const uint32_t idesc_s = idesc_f32acc(1, 1, 256, kTile, 0, 0);
-      const uint32_t idesc_o = idesc_f32acc(1, 1, 256, 256, 0, 1);
-      const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem));
-      const uint64_t k_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffRing));
-      const uint64_t v_desc = sdesc_mnmajor_sw128(smem_u32(smem + kOffRing), 8192, 1024);
+    // ------------------------------------------------------------------ MMA issue: one thread of each leader
+    if (side == 0 && elect_one()) {
       int slot = 0, piece = 0;
       uint32_t ph = 0, g = 0;             // ring phase, tiles so far
       bool ok = true;
@@ -381,134 +389,270 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
       };
-      auto qk = [&](uint32_t buf, bool first) {
-        const uint32_t d = tmem + kTmemS + buf * kTile;
-#pragma unroll
-        for (int f = 0; f < 9; f += 2) {
-          if (ok && first && !mbar_wait(&q_full[f / 2], piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q)) ok = false;
-          if (ok) wait_full();
-          if (!ok) break;
-          const uint64_t a = q_desc + (uint64_t)((f * kQBlock) >> 4), b = k_desc + (uint64_t)((slot * kSlot) >> 4);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (f + (k >> 2) < 9)
-              pair_mma_ss(d, a + 2 * (k & 3) + (k >> 2) * (kQBlock >> 4), b + 2 * (k & 3) + (k >> 2) * (8192 >> 4), idesc_s,
-                          (f | k) != 0);
-          pair_commit(&empty[slot]);
-          advance();
-        }
-        if (ok) pair_commit(&s_full[buf]);
-      };
-      for (; ok && w.valid(); w.next(p)) {
-        Tile cur = get_tile(p, w.x, w.t0);
-        if (cur.most() == 0) continue;
-        bool startedA = false, startedB = false;
-        qk(g & 1, true);
-        for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-          if (t + 1 < w.t1) qk((g + 1) & 1, false);
-          else pair_commit(q_empty);
-          if (!ok) break;
-          cur = get_tile(p, w.x, t);
-          // the token that sees nothing of the tile keeps its O
-          const uint32_t off0 = cur.nA > 0 ? 0u : 0xffffffffu, off1 = cur.nB > 0 ? 0u : 0xffffffffu;
-          bool acc = (cur.nA > 0 && startedA) || (cur.nB > 0 && startedB);
-          startedA |= cur.nA > 0;
-          startedB |= cur.nB > 0;
-          const int n = cur.most();
-          const uint32_t a = tmem + kTmemS + (g & 1) * kTile;
-          if (t == w.t0 && piece > 0 && !mbar_wait(o_free, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O))
-            ok = false;
-          if (!ok || !mbar_wait(&p_full[g & 1], (g >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) ok = false;
+      if (!values) {
+        const uint32_t idesc = idesc_f32acc(1, 1, 256, kTile, 0, 0);
+        const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(ring);
+        for (; ok && w.valid(); w.next(p)) {
+          if (w.empty(p)) continue;
+          if (!mbar_wait(q_full, piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q)) break;
           tc_fence_after();
-          for (int kb = 0; ok && kb < n; kb += 64) {
-            wait_full();
-            if (!ok) break;
-            const bool part = n - kb < 64;
-            if (cur.src >= 0 && part) cluster_fence();               // both CTAs' warps wrote this slot
-            const uint64_t b = v_desc + (uint64_t)((slot * kSlot) >> 4);
-            if ((off0 | off1) == 0 && !part) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) pair_mma_ts(tmem, a + kb / 2 + 8 * k, b + 128 * k, idesc_o, acc || k > 0);
-            } else {
-              for (int k = 0; k < 4 && kb + 16 * k < n; ++k)
-                pair_mma_ts_masked(tmem, a + kb / 2 + 8 * k, b + 128 * k, idesc_o, off0, off1, acc || k > 0);
+          for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+            const uint32_t buf = g & 1, d = tmem + kTmemS + buf * kTile;
+            if (!mbar_wait(&s_free[buf], ((g >> 1) + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_S)) {
+              ok = false;
+              break;
             }
-            pair_commit(&empty[slot]);
-            acc = true;
-            advance();
+#pragma unroll
+            for (int f = 0; f < 9; f += 2) {
+              if (ok) wait_full();
+              if (!ok) break;
+              const uint64_t b = k_desc + (uint64_t)((slot * kBlock) >> 4);
+              if (f < 8) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  pair_mma_ts(d, tmem + 32 * f + 8 * k, b + 2 * (k & 3) + (k >> 2) * (8192 >> 4), idesc, (f | k) != 0);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) pair_mma_ss(d, q_desc + 2 * k, b + 2 * k, idesc, 1);
+              }
+              pair_commit(&empty[slot], 3);
+              advance();
+            }
+            if (ok) pair_commit(&s_full[buf], 3);
           }
-          if (ok) pair_commit(&pv_done[g & 1]);
+          if (ok) pair_commit(q_empty, 3);
+          ++piece;
         }
-        ++piece;
+      } else {
+        const uint32_t idesc = idesc_f32acc(1, 1, 256, 256, 0, 1);
+        const uint64_t p_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffP)), v_desc = sdesc_mnmajor_sw128(ring, 8192, 1024);
+        for (; ok && w.valid(); w.next(p)) {
+          if (w.empty(p)) continue;
+          bool startedA = false, startedB = false;
+          if (piece > 0 && !mbar_wait(o_free, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O)) break;
+          for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+            const Tile tile = get_tile(p, w.x, t);
+            // the token that sees nothing of the tile keeps its O
+            const uint32_t off0 = tile.nA > 0 ? 0u : 0xffffffffu, off1 = tile.nB > 0 ? 0u : 0xffffffffu;
+            const bool acc = (tile.nA > 0 && startedA) || (tile.nB > 0 && startedB);
+            startedA |= tile.nA > 0;
+            startedB |= tile.nB > 0;
+            const int n = tile.most();
+            if (!mbar_wait(&p_ready[g & 1], (g >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            for (int i = 0; ok && 64 * (i >> 1) < n; ++i) {
+              const int kb = 64 * (i >> 1);
+              wait_full();
+              if (!ok) break;
+              const bool part = n - kb < 64;
+              if (tile.src >= 0 && part) cluster_fence();            // both CTAs' warps wrote this slot
+              const uint32_t d = tmem + 256 * (i & 1);
+              const uint64_t a = p_desc + (uint64_t)(((2 * (g & 1) + (i >> 1)) * kBlock) >> 4);
+              const uint64_t b = v_desc + (uint64_t)((slot * kBlock) >> 4);
+              if ((off0 | off1) == 0 && !part) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) pair_mma_ss(d, a + 2 * k, b + 128 * k, idesc, acc || kb + k > 0);
+              } else {
+                for (int k = 0; k < 4 && kb + 16 * k < n; ++k)
+                  pair_mma_ss_masked(d, a + 2 * k, b + 128 * k, idesc, off0, off1, acc || kb + k > 0);
+              }
+              pair_commit(&empty[slot], 12);
+              advance();
+            }
+            if (ok) pair_commit(&pv_done[g & 1], 15);
+          }
+          ++piece;
+        }
       }
     }
-  } else if (warp >= 4) {
+  } else if (!values && warp < 8) {
     // ------------------------------------------------------------------ softmax, one thread per row
-    const int row = tid - 128;            // head; TMEM lane
-    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int row = tid - 128, quad = warp & 3;            // head; TMEM lane
+    const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t peer = rank + 2;
     uint32_t g = 0;
+    int piece = 0;
     bool ok = true;
     int32_t info_cont = -1, info_head = -1;
     for (; ok && w.valid(); w.next(p)) {
-      const int tok = 2 * w.u + (int)rank;
+      const int tok = 2 * w.u + (int)side;
+      const bool some = !w.empty(p);
       float m = -INFINITY, l = 0.f;
-      bool any = false;
-      for (int t = w.t0; ok && t < w.t1; ++t) {
+      for (int t = w.t0; some && ok && t < w.t1; ++t, ++g) {
         const Tile tile = get_tile(p, w.x, t);
-        if (tile.most() == 0) continue;
-        const int n = rank == 0 ? tile.nA : tile.nB;
+        const int n = side == 0 ? tile.nA : tile.nB;
         const uint32_t buf = g & 1, ph = (g >> 1) & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], ph, &abort_flag, p.status, DSA_SITE_SHARED_S))) {
           ok = false;
           break;
         }
         tc_fence_after();
+        uint32_t r[4][32];
         if (n > 0) {
-          uint32_t r[4][32];
-          const uint32_t s = t_row + kTmemS + buf * kTile;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s + 32 * c, r[c]);
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_row + kTmemS + buf * kTile + 32 * c, r[c]);
           tmem_ld_wait();
-          if (n < kTile) {
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(cluster_addr(&s_free[buf], 0));
+        // the staging buffer, and the value CTA's, held the tile before the last
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[buf], ph ^ 1, &abort_flag, p.status, DSA_SITE_SHARED_P))) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = cluster_addr(&p_full[buf], peer);
+        if (n == 0) {
+          if (lane == 0) arrive_cluster(bar);
+          continue;
+        }
+        if (n < kTile) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * c + i >= n) r[c][i] = 0xff800000u;
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i >= n) r[c][i] = 0xff800000u;
+        }
+        float mx4[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx4[c] = __uint_as_float(r[c][0]);
+#pragma unroll
+          for (int i = 1; i < 32; ++i) mx4[c] = fmaxf(mx4[c], __uint_as_float(r[c][i]));
+        }
+        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
+        float alpha = 1.f;
+        if (mx > m + kRescale) {
+          if (m != -INFINITY) alpha = exp2_approx(m - mx);
+          m = mx;
+        }
+        const float mm = m == -INFINITY ? 0.f : m;         // every score -inf: e^-inf = 0, not NaN
+        float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t stage = smem_u32(smem + kOffP) + buf * 2 * kBlock + row * 128;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {                      // eight keys, 16 bytes
+          uint32_t pk[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float e0 = exp2_approx(fmaf(__uint_as_float(r[c >> 2][(c & 3) * 8 + 2 * i]), p.scale_log2, -mm));
+            const float e1 = exp2_approx(fmaf(__uint_as_float(r[c >> 2][(c & 3) * 8 + 2 * i + 1]), p.scale_log2, -mm));
+            sum4[i] += e0 + e1;
+            pk[i] = pack_bf16(e0, e1);
           }
-          float mx4[4];
+          st_shared_16(stage + (c >> 3) * kBlock + (((c & 7) ^ (row & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+        }
+        l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
+        alpha_sm[buf * 128 + row] = alpha;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) {
+          arrive_expect_tx_cluster(bar, 2 * 4096 + 128);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            mx4[c] = __uint_as_float(r[c][0]);
-#pragma unroll
-            for (int i = 1; i < 32; ++i) mx4[c] = fmaxf(mx4[c], __uint_as_float(r[c][i]));
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* src = smem + kOffP + (2 * buf + i) * kBlock + quad * 4096;
+            copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 4096, bar);
           }
-          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
-          float alpha = 1.f;
-          bool rescale = false;
-          if (mx > m + kRescale) {
-            alpha = exp2_approx(m - mx);  // 0 for the first
-            rescale = m != -INFINITY;
-            m = mx;
-          }
-          const float mm = m == -INFINITY ? 0.f : m;   // every score -inf: e^-inf = 0, not NaN
-          float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t pk[2][32];
+          const float* src = alpha_sm + buf * 128 + 32 * quad;
+          copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 128, bar);
+        }
+      }
+      if (!ok) break;
+      if (some) {
+        // the row's sum, for the value CTA (four buffers: it may still be two pieces behind)
+        const int i = piece & 3;
+        l_sm[i * 128 + row] = l;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) {
+          const uint32_t bar = cluster_addr(&l_full[i], peer);
+          arrive_expect_tx_cluster(bar, 128);
+          const float* src = l_sm + i * 128 + 32 * quad;
+          copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 128, bar);
+        }
+        ++piece;
+      }
+      const bool whole = w.t0 == 0 && w.t1 == w.x.tiles;
+      const int where = w.t0 == 0 ? 1 : 0;
+      if (whole) {
+        if (tok < p.BT && p.lse) p.lse[(int64_t)tok * kHeads + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        (where ? info_head : info_cont) = w.u;
+        const int64_t slot = (int64_t)cluster * 2 + where;
+        *reinterpret_cast<float2*>(p.part_ml + (slot * 256 + (int)side * kHeads + row) * 2) = make_float2(m, l);
+      }
+    }
+    for (uint32_t i = g > 2 ? g - 2 : 0; ok && i < g; ++i)   // as in the loads: the last arrivals
+      if (!mbar_wait(&pv_done[i & 1], (i >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) ok = false;
+    if (rank == 0 && tid == 128) {
+      p.info[2 * cluster] = info_cont;
+      p.info[2 * cluster + 1] = info_head;
+    }
+  } else if (!values) {
+    // ------------------------------------------------------------------ Q features 0..511 into TMEM, one thread per row
+    const int row = tid - 256;
+    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    int piece = 0;
+    for (; w.valid(); w.next(p)) {
+      if (w.empty(p)) continue;
+      const int tok = 2 * w.u + (int)side;
+      const bool there = tok < p.BT;                       // else a row of zeros
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(there ? tok : 0) * kHeads + row) * kDqk);
+      if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status,
+                                                          DSA_SITE_SHARED_EMPTY)))
+        break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 8; c += 2) {
+        uint4 v[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+        for (int i = 0; i < 16; ++i) v[i] = there ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float e0 = exp2_approx(fmaf(__uint_as_float(r[c][i]), p.scale_log2, -mm));
-              const float e1 = exp2_approx(fmaf(__uint_as_float(r[c][i + 1]), p.scale_log2, -mm));
-              sum4[(i >> 1) & 3] += e0 + e1;
-              pk[c >> 1][(c & 1) * 16 + i / 2] = pack_bf16(e0, e1);
-            }
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[4 * i] = v[8 * h + i].x;
+            x[4 * i + 1] = v[8 * h + i].y;
+            x[4 * i + 2] = v[8 * h + i].z;
+            x[4 * i + 3] = v[8 * h + i].w;
           }
-          l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
-          if (__any_sync(0xffffffffu, rescale)) {
+          tmem_st32(t_row + 32 * (c + h), x);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(cluster_addr(q_full, 0));
+      ++piece;
+    }
+  } else {
+    // ------------------------------------------------------------------ O: rescaling and output; one thread per row and
+    // half of the features
+    const int row = (tid - 128) & 127, half = (tid - 128) >> 7;
+    const uint32_t t_o = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 * half;
+    uint32_t g = 0;
+    int piece = 0;
+    bool ok = true;
+    for (; ok && w.valid(); w.next(p)) {
+      const int tok = 2 * w.u + (int)side;
+      const bool some = !w.empty(p);
+      bool any = false;                                    // O of this token holds something
+      for (int t = w.t0; some && ok && t < w.t1; ++t, ++g) {
+        const Tile tile = get_tile(p, w.x, t);
+        const uint32_t buf = g & 1, ph = (g >> 1) & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait(&p_full[buf], ph, &abort_flag, p.status, DSA_SITE_SHARED_P))) {
+          ok = false;
+          break;
+        }
+        if ((side == 0 ? tile.nA : tile.nB) > 0) {
+          const float alpha = any ? alpha_sm[buf * 128 + row] : 1.f;
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
             // P V of every earlier tile has to be in O first
-            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag,
-                                                           p.status, DSA_SITE_SHARED_O))) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status,
+                                                   DSA_SITE_SHARED_O))) {
               ok = false;
               break;
             }
@@ -516,113 +660,105 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
               uint32_t o[32];
-              tmem_ld32(t_row + 32 * c, o);
+              tmem_ld32(t_o + 32 * c, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * (rescale ? alpha : 1.f));
-              tmem_st32(t_row + 32 * c, o);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(t_o + 32 * c, o);
             }
+            tmem_st_wait();
+            tc_fence_before();
           }
           any = true;
-          tmem_st32(s, pk[0]);
-          tmem_st32(s + 32, pk[1]);
-          tmem_st_wait();
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(leader_addr(&p_full[buf]));
-        ++g;
+        if (lane == 0) arrive_cluster(cluster_addr(&p_ready[buf], 2));
       }
       if (!ok) break;
-      // ---- the piece is done: output, or a partial for the join
       const bool whole = w.t0 == 0 && w.t1 == w.x.tiles;
-      const int where = w.t0 == 0 ? 1 : 0;
-      if (!whole) (where ? info_head : info_cont) = 2 * w.u + w.half;
-      const bool had = get_tile(p, w.x, w.t0).most() > 0;
-      if (had) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status,
-                                                       DSA_SITE_SHARED_O))) {
+      float l = 0.f;
+      if (some) {
+        const bool there = mbar_wait(&l_full[piece & 3], (piece >> 2) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P) &&
+                           mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O);
+        if (!__all_sync(0xffffffffu, there)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        l = l_sm[(piece & 3) * 128 + row];
+        ++piece;
       }
-      const int64_t slot = (int64_t)pair * 2 + where;
-      const int prow = (int)rank * kHeads + row;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      if (whole) {
-        if (tok < p.BT && w.half == 0 && p.lse)
-          p.lse[(int64_t)tok * kHeads + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      } else {
-        *reinterpret_cast<float2*>(p.part_ml + (slot * 256 + prow) * 2) = make_float2(m, l);
-      }
+      const int64_t slot = (int64_t)cluster * 2 + (w.t0 == 0 ? 1 : 0);
+      const int prow = (int)side * kHeads + row;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        uint32_t o[32];
+      for (int c = 0; c < 8; c += 2) {
+        uint32_t o[2][32];
         if (any) {
-          tmem_ld32(t_row + 32 * c, o);
+          tmem_ld32(t_o + 32 * c, o[0]);
+          tmem_ld32(t_o + 32 * c + 32, o[1]);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = 0u;
+          for (int i = 0; i < 32; ++i) o[0][i] = o[1][i] = 0u;
         }
         if (whole) {
           if (tok < p.BT) {
-            uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)tok * kHeads + row) * kDv + 256 * w.half + 32 * c);
+            uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)tok * kHeads + row) * kDv + 256 * half + 32 * c);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t* y = &o[i >> 2][8 * (i & 3)];
               uint4 v;
-              v.x = pack_bf16(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
-              v.y = pack_bf16(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
-              v.z = pack_bf16(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
-              v.w = pack_bf16(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
+              v.x = pack_bf16(__uint_as_float(y[0]) * inv, __uint_as_float(y[1]) * inv);
+              v.y = pack_bf16(__uint_as_float(y[2]) * inv, __uint_as_float(y[3]) * inv);
+              v.z = pack_bf16(__uint_as_float(y[4]) * inv, __uint_as_float(y[5]) * inv);
+              v.w = pack_bf16(__uint_as_float(y[6]) * inv, __uint_as_float(y[7]) * inv);
               dst[i] = v;
             }
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (slot * 64 + 8 * c) * 256 + prow;
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o) + (slot * 128 + 64 * half + 8 * c) * 256 + prow;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i * 256] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t* y = &o[i >> 3][4 * (i & 7)];
+            dst[i * 256] = make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
       }
-      if (had) {
+      if (some) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_cluster(leader_addr(o_free));
+        if (lane == 0) arrive_cluster(cluster_addr(o_free, 2));
       }
-    }
-    if (rank == 0 && tid == 128) {
-      p.info[2 * pair] = info_cont;
-      p.info[2 * pair + 1] = info_head;
     }
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  pair_barrier();                        // nothing of the pair is still in flight towards either CTA
+  cluster_arrive();                      // nothing of the cluster is in flight towards a CTA that has left
+  cluster_wait();
   if (warp == 2) pair_tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of items that were cut: block (p, y) takes 32 rows x 64 features of the item whose
-// first piece is the last one of pair p; the pieces that follow are the first ones of the next pairs.
-__global__ void __launch_bounds__(256) mla_shared_join_kernel(const SharedParams p, int pairs) {
+// Joins the pieces of units that were cut: block (c, y) takes 32 rows x 64 features of the unit whose
+// first piece is the last one of cluster c; the pieces that follow are the first ones of the next.
+__global__ void __launch_bounds__(256) mla_shared_join_kernel(const SharedParams p, int clusters) {
   extern __shared__ float2 ml_sh[];      // [pieces][32 rows]: maximum, sum
-  const int pair = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  const int item = __ldcg(p.info + 2 * pair + 1);
-  if (item < 0) return;
-  const int row = (blockIdx.y >> 2) * 32 + lane, col = (blockIdx.y & 3) * 64 + 8 * warp;
-  const int tok = 2 * (item >> 1) + (row >> 7);
-  const int head = row & 127, half = item & 1;
+  const int unit = __ldcg(p.info + 2 * c + 1);
+  if (unit < 0) return;
+  const int row = (blockIdx.y >> 3) * 32 + lane, col = (blockIdx.y & 7) * 64 + 8 * warp;
+  const int tok = 2 * unit + (row >> 7), head = row & 127;
   if (tok >= p.BT) return;               // the same for the whole block
   int n = 1;                             // pieces
-  for (int q = pair + 1; q < pairs; q += 32) {
-    const uint32_t other = __ballot_sync(0xffffffffu, q + lane >= pairs || __ldcg(p.info + 2 * (q + lane)) != item);
+  for (int q = c + 1; q < clusters; q += 32) {
+    const uint32_t other = __ballot_sync(0xffffffffu, q + lane >= clusters || __ldcg(p.info + 2 * (q + lane)) != unit);
     n += other ? __ffs(other) - 1 : 32;
     if (other) break;
   }
-  auto slot_of = [&](int i) { return i == 0 ? (int64_t)pair * 2 + 1 : (int64_t)(pair + i) * 2; };
+  auto slot_of = [&](int i) { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
   for (int i = warp; i < n; i += 8)
     ml_sh[i * 32 + lane] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(i) * 256 + row);
   __syncthreads();
@@ -638,7 +774,7 @@ __global__ void __launch_bounds__(256) mla_shared_join_kernel(const SharedParams
     l += ml.y * f;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float4 v = __ldcg(src + slot_of(i) * (64 * 256) + j * 256);
+      const float4 v = __ldcg(src + slot_of(i) * (128 * 256) + j * 256);
       acc[j].x = fmaf(v.x, f, acc[j].x);
       acc[j].y = fmaf(v.y, f, acc[j].y);
       acc[j].z = fmaf(v.z, f, acc[j].z);
@@ -647,20 +783,51 @@ __global__ void __launch_bounds__(256) mla_shared_join_kernel(const SharedParams
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int64_t out_row = (int64_t)tok * kHeads + head;
-  *reinterpret_cast<uint4*>(p.out + out_row * kDv + 256 * half + col) =
+  *reinterpret_cast<uint4*>(p.out + out_row * kDv + col) =
       make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
                  pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
-  if (col == 0 && half == 0 && p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (col == 0 && p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 namespace {
 
-// Pairs of the launch: one per two SMs, at most one per tile.
-int shared_pairs(int64_t BT, int T, int P, int S_max) {
+// Clusters of four that the device holds at once, one CTA per SM (33 on a B200: its SM groups do not
+// all divide by four). More would wait for a second wave.
+int resident_clusters() {
+  static uint64_t seen[dsa_host::kMaxSetupDevices];
+  static int count[dsa_host::kMaxSetupDevices];
+  int dev = 0;
+  if (!dsa_host::needs_setup(seen, &dev)) return count[dev];
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(dsa_host::device_sm_count() / 4 * 4));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 4;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(mla_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, mla_shared_kernel, &cfg) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return dsa_host::device_sm_count() / 4;              // no device here: the most there can be
+  }
+  if (dev >= 0 && dev < dsa_host::kMaxSetupDevices) {
+    count[dev] = n;
+    dsa_host::mark_setup(seen);
+  }
+  return n;
+}
+
+// Clusters of the launch, at most one per tile.
+int shared_clusters(int64_t BT, int P, int S_max) {
   const int64_t units = (BT + 1) / 2;
   const int64_t own = (S_max + kTile - 1) / kTile;
   const int64_t tiles = std::max<int64_t>(1, (P + kTile - 1) / kTile + 2 * own);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(dsa_host::device_sm_count() / 2, 2 * units * tiles));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(resident_clusters(), units * tiles));
 }
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -668,8 +835,8 @@ size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 }  // namespace
 
 size_t mla_shared_workspace_size(int B, int T, int P, int S_max) {
-  const size_t pairs = (size_t)shared_pairs((int64_t)B * T, T, P, S_max);
-  return align256(pairs * 8) + pairs * 2 * 256 * 8 + pairs * 2 * 64 * 256 * 16;
+  const size_t n = (size_t)shared_clusters((int64_t)B * T, P, S_max);
+  return align256(n * 8) + n * 2 * 256 * 8 + n * 2 * 128 * 256 * 16;
 }
 
 int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const uint16_t* kv, const int32_t* q_pos,
@@ -677,6 +844,7 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
                       void* workspace, size_t ws_bytes, cudaStream_t stream, int* status) {
   if (!workspace || ws_bytes < mla_shared_workspace_size(B, T, P, S_max)) return DSA_ERR_WORKSPACE;
   SharedParams p;
+  p.q = q;
   p.kv = kv;
   p.q_pos = q_pos;
   p.kv_len = kv_len;
@@ -688,12 +856,12 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
   p.out = out;
   p.lse = lse;
   p.status = status;
-  const int pairs = shared_pairs(p.BT, T, P, S_max);
+  const int clusters = shared_clusters(p.BT, P, S_max);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.info = reinterpret_cast<int32_t*>(ws);
-  ws += align256((size_t)pairs * 8);
+  ws += align256((size_t)clusters * 8);
   p.part_ml = reinterpret_cast<float*>(ws);
-  ws += (size_t)pairs * 2 * 256 * 8;
+  ws += (size_t)clusters * 2 * 256 * 8;
   p.part_o = reinterpret_cast<float*>(ws);
 
   const auto dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -714,15 +882,10 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
     const uint64_t dims[4] = {64, (uint64_t)S_max, 9, (uint64_t)B}, strides[3] = {row, 128, row * (uint64_t)S_max};
     if (!dsa_host::encode_tensor_map(&sm, dt, 4, const_cast<uint16_t*>(kv), dims, strides, box, sw)) return DSA_ERR_CUDA;
   }
-  static uint64_t seen[dsa_host::kMaxSetupDevices];
-  if (dsa_host::needs_setup(seen, nullptr)) {
-    if (cudaFuncSetAttribute(mla_shared_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess)
-      return DSA_ERR_CUDA;
-    dsa_host::mark_setup(seen);
-  }
-  int rc = dsa_host::launch_pairs(mla_shared_kernel, (unsigned)pairs, kThreads, kSmem, stream, q_map, pm, sm, p);
+  int rc = dsa_host::launch_clusters(mla_shared_kernel, 4, (unsigned)clusters, kThreads, kSmem, stream, q_map, pm, sm, p);
   if (rc != DSA_OK) return rc;
-  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)pairs, 32), dim3(256), (size_t)pairs * 32 * 8, stream, p, pairs);
+  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)clusters, 64), dim3(256), (size_t)clusters * 32 * 8, stream,
+                          p, clusters);
 }
 
 }  // namespace dsa

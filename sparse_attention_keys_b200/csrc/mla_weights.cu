@@ -251,6 +251,8 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
         }
         if (ok) mma_commit(q_empty);
       }
+      // the last arrivals have to reach this CTA before it leaves
+      if (ok && run > 0) mbar_wait(q_empty, (run + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ gather (selected rows)

@@ -1,5 +1,5 @@
-// Device helpers for kernels that run as pairs of CTAs (clusters of two) on one tcgen05 matrix
-// product (cta_group::2): CTA 0 of the pair, the leader, issues every MMA; each CTA holds its own
+// Device helpers for kernels whose CTAs work in pairs (ranks 2i and 2i + 1 of a cluster) on one tcgen05
+// matrix product (cta_group::2): the lower rank, the leader, issues every MMA; each CTA holds its own
 // 128 rows of A and D (its shared memory and TMEM) and half of the N rows of B.
 #pragma once
 
@@ -7,27 +7,23 @@
 
 namespace dsa {
 
-__device__ __forceinline__ uint32_t pair_rank() {
+__device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
 
-// The shared::cluster address of the leader's copy of this CTA's shared-memory object.
-__device__ __forceinline__ uint32_t leader_addr(const void* p) {
+// The shared::cluster address of the same shared-memory object in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   uint32_t o;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(o) : "r"(smem_u32(p)));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(o) : "r"(smem_u32(p)), "r"(rank));
   return o;
 }
 
-__device__ __forceinline__ void pair_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The two halves of pair_barrier: what a thread wrote before pair_arrive is seen by both CTAs after
-// every thread's pair_wait.
-__device__ __forceinline__ void pair_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void pair_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The two halves of a cluster barrier: what a thread wrote before cluster_arrive is seen by every CTA
+// after cluster_wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 // One thread of a converged warp (the compiler then keeps the MMA operands in uniform registers).
 __device__ __forceinline__ bool elect_one() {
@@ -84,13 +80,13 @@ __device__ __forceinline__ void pair_tmem_dealloc(uint32_t taddr, uint32_t ncols
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
 
-// One arrival on the barrier at this shared-memory offset in both CTAs once every MMA issued so far
-// by this thread has completed.
-__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+// One arrival on the barrier at this shared-memory offset in the CTAs of the cluster whose bit is set
+// in `ranks`, once every MMA issued so far by this thread has completed.
+__device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t ranks) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"(ranks)
       : "memory");
 }
 
@@ -112,14 +108,28 @@ __device__ __forceinline__ void pair_mma_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// A in TMEM; the rows of CTA 0 (off0 = ~0) or of CTA 1 (off1 = ~0) of D stay as they are.
-__device__ __forceinline__ void pair_mma_ts_masked(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+// A in shared memory; the rows of the first CTA (off0 = ~0) or of the second (off1 = ~0) of D stay as
+// they are.
+__device__ __forceinline__ void pair_mma_ss_masked(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                                    uint32_t off0, uint32_t off1, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, {%4, %4, %4, %4, %5, %5, %5, %5}, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(off0), "r"(off1), "r"(accumulate)
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%4, %4, %4, %4, %5, %5, %5, %5}, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(off0), "r"(off1), "r"(accumulate)
       : "memory");
+}
+
+// Copies `bytes` (a multiple of 16) of this CTA's shared memory to a shared::cluster address; they
+// complete on the barrier `bar` (a shared::cluster address) of the receiving CTA. The source has to be
+// visible to the async proxy (fence_proxy_async_smem).
+__device__ __forceinline__ void copy_to_cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_shared_16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // 2^x with the MUFU approximation (relative error about 2^-22)
@@ -132,11 +142,12 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }  // namespace dsa
 
 namespace dsa_host {
-// launch() for a grid of CTA pairs.
+// launch() for a grid of `clusters` clusters of `size` CTAs.
 template <typename... KArgs, typename... Args>
-int launch_pairs(void (*kernel)(KArgs...), unsigned pairs, unsigned threads, size_t smem, cudaStream_t stream, Args... args) {
+int launch_clusters(void (*kernel)(KArgs...), unsigned size, unsigned clusters, unsigned threads, size_t smem,
+                    cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * pairs);
+  cfg.gridDim = dim3(size * clusters);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -144,7 +155,7 @@ int launch_pairs(void (*kernel)(KArgs...), unsigned pairs, unsigned threads, siz
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = size;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
