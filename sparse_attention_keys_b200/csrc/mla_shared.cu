@@ -48,10 +48,11 @@ constexpr int kOffP = kBlock;                      // [2][2 blocks of 64 keys]: 
 constexpr int kOffRing = kOffP + 4 * kBlock;       // [0, kBlock): Q features 512..575
 constexpr int kOffAlpha = kOffRing + kSlots * kBlock;   // [2][128] fp32
 constexpr int kOffL = kOffAlpha + 2 * 128 * 4;     // [4][128] fp32
-constexpr int kOffBar = kOffL + 4 * 128 * 4;
+constexpr int kOffMax = kOffL + 4 * 128 * 4;       // [2][2][128] fp32
+constexpr int kOffBar = kOffMax + 4 * 128 * 4;
 constexpr int kSmem = 1024 + kOffBar + 512;
 static_assert(kSmem + 1024 <= 232448, "shared memory per CTA");
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr uint32_t kTmemS = 256;                   // score CTA: Q in [0, 256), scores in 2 x 128 columns
 constexpr float kLn2 = 0.69314718055994530942f;
 // The running maximum moves, and O is rescaled, only when a tile exceeds it by 2^32: P stays below
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   float* alpha_sm = reinterpret_cast<float*>(smem + kOffAlpha);
   float* l_sm = reinterpret_cast<float*>(smem + kOffL);
+  float* max_sm = reinterpret_cast<float*>(smem + kOffMax);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* full = bars;                 // leader of each pair [kSlots]: both CTAs' parts of the slot have landed
   uint64_t* empty = full + kSlots;       // both of a pair [kSlots]: the MMAs that read the slot are done
@@ -209,8 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 8);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&s_free[i], 16);
+      mbar_init(&p_full[i], 8);
       mbar_init(&p_ready[i], 16);
       mbar_init(&pv_done[i], 1);
     }
@@ -468,19 +470,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (!values && warp < 8) {
-    // ------------------------------------------------------------------ softmax, one thread per row
-    const int row = tid - 128, quad = warp & 3;            // head; TMEM lane
-    const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16);
+  } else if (!values && warp < 12) {
+    // ------------------------------------------------------------------ softmax: two threads per row, 64 keys each
+    // (one thread per row took 3500 cycles a tile, more than the tile's MMAs)
+    const int row = (tid - 128) & 127, half = (tid - 128) >> 7, quad = warp & 3;     // row: head, TMEM lane
+    const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16) + 64 * half;
     const uint32_t peer = rank + 2;
     uint32_t g = 0;
     int piece = 0;
     bool ok = true;
     int32_t info_cont = -1, info_head = -1;
+    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };   // the two warps of these rows
     for (; ok && w.valid(); w.next(p)) {
       const int tok = 2 * w.u + (int)side;
       const bool some = !w.empty(p);
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;                        // l: of this thread's keys
       for (int t = w.t0; some && ok && t < w.t1; ++t, ++g) {
         const Tile tile = get_tile(p, w.x, t);
         const int n = side == 0 ? tile.nA : tile.nB;
@@ -490,50 +494,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        uint32_t r[4][32];
+        uint32_t r[2][32];
         if (n > 0) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(t_row + kTmemS + buf * kTile + 32 * c, r[c]);
+          tmem_ld32(t_row + kTmemS + buf * kTile, r[0]);
+          tmem_ld32(t_row + kTmemS + buf * kTile + 32, r[1]);
           tmem_ld_wait();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(cluster_addr(&s_free[buf], 0));
+        const uint32_t bar = cluster_addr(&p_full[buf], peer);
+        float alpha = 1.f, mm = 0.f;
+        if (n > 0) {
+          if (n < kTile) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (64 * half + 32 * c + i >= n) r[c][i] = 0xff800000u;
+          }
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(r[c][i]));
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          max_sm[(2 * buf + half) * 128 + row] = mx;
+          pair_sync();
+          mx = fmaxf(mx, max_sm[(2 * buf + (half ^ 1)) * 128 + row]) * p.scale_log2;
+          if (mx > m + kRescale) {
+            if (m != -INFINITY) alpha = exp2_approx(m - mx);
+            m = mx;
+          }
+          mm = m == -INFINITY ? 0.f : m;                   // every score -inf: e^-inf = 0, not NaN
+        }
         // the staging buffer, and the value CTA's, held the tile before the last
         if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[buf], ph ^ 1, &abort_flag, p.status, DSA_SITE_SHARED_P))) {
           ok = false;
           break;
         }
-        const uint32_t bar = cluster_addr(&p_full[buf], peer);
         if (n == 0) {
           if (lane == 0) arrive_cluster(bar);
           continue;
         }
-        if (n < kTile) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= n) r[c][i] = 0xff800000u;
-        }
-        float mx4[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx4[c] = __uint_as_float(r[c][0]);
-#pragma unroll
-          for (int i = 1; i < 32; ++i) mx4[c] = fmaxf(mx4[c], __uint_as_float(r[c][i]));
-        }
-        const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
-        float alpha = 1.f;
-        if (mx > m + kRescale) {
-          if (m != -INFINITY) alpha = exp2_approx(m - mx);
-          m = mx;
-        }
-        const float mm = m == -INFINITY ? 0.f : m;         // every score -inf: e^-inf = 0, not NaN
         float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-        const uint32_t stage = smem_u32(smem + kOffP) + buf * 2 * kBlock + row * 128;
+        uint8_t* stage = smem + kOffP + (2 * buf + half) * kBlock;
+        const uint32_t stage_row = smem_u32(stage) + row * 128;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {                      // eight keys, 16 bytes
+        for (int c = 0; c < 8; ++c) {                      // eight keys, 16 bytes
           uint32_t pk[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -542,46 +550,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum4[i] += e0 + e1;
             pk[i] = pack_bf16(e0, e1);
           }
-          st_shared_16(stage + (c >> 3) * kBlock + (((c & 7) ^ (row & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+          st_shared_16(stage_row + ((c ^ (row & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
         }
         l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
-        alpha_sm[buf * 128 + row] = alpha;
+        if (half == 0) alpha_sm[buf * 128 + row] = alpha;
         fence_proxy_async_smem();
         __syncwarp();
         if (elect_one()) {
-          arrive_expect_tx_cluster(bar, 2 * 4096 + 128);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint8_t* src = smem + kOffP + (2 * buf + i) * kBlock + quad * 4096;
-            copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 4096, bar);
+          arrive_expect_tx_cluster(bar, half == 0 ? 4096 + 128 : 4096);
+          const uint8_t* src = stage + quad * 4096;
+          copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 4096, bar);
+          if (half == 0) {
+            const float* factors = alpha_sm + buf * 128 + 32 * quad;
+            copy_to_cluster(cluster_addr(factors, peer), smem_u32(factors), 128, bar);
           }
-          const float* src = alpha_sm + buf * 128 + 32 * quad;
-          copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 128, bar);
         }
       }
       if (!ok) break;
       if (some) {
         // the row's sum, for the value CTA (four buffers: it may still be two pieces behind)
         const int i = piece & 3;
-        l_sm[i * 128 + row] = l;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (elect_one()) {
-          const uint32_t bar = cluster_addr(&l_full[i], peer);
-          arrive_expect_tx_cluster(bar, 128);
-          const float* src = l_sm + i * 128 + 32 * quad;
-          copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 128, bar);
+        if (half == 1) l_sm[i * 128 + row] = l;
+        pair_sync();
+        if (half == 0) {
+          l += l_sm[i * 128 + row];
+          l_sm[i * 128 + row] = l;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (elect_one()) {
+            const uint32_t bar = cluster_addr(&l_full[i], peer);
+            arrive_expect_tx_cluster(bar, 128);
+            const float* src = l_sm + i * 128 + 32 * quad;
+            copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 128, bar);
+          }
         }
         ++piece;
       }
       const bool whole = w.t0 == 0 && w.t1 == w.x.tiles;
       const int where = w.t0 == 0 ? 1 : 0;
-      if (whole) {
-        if (tok < p.BT && p.lse) p.lse[(int64_t)tok * kHeads + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      } else {
-        (where ? info_head : info_cont) = w.u;
-        const int64_t slot = (int64_t)cluster * 2 + where;
-        *reinterpret_cast<float2*>(p.part_ml + (slot * 256 + (int)side * kHeads + row) * 2) = make_float2(m, l);
+      if (!whole) (where ? info_head : info_cont) = w.u;
+      if (half == 0) {
+        if (whole) {
+          if (tok < p.BT && p.lse) p.lse[(int64_t)tok * kHeads + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        } else {
+          const int64_t slot = (int64_t)cluster * 2 + where;
+          *reinterpret_cast<float2*>(p.part_ml + (slot * 256 + (int)side * kHeads + row) * 2) = make_float2(m, l);
+        }
       }
     }
     for (uint32_t i = g > 2 ? g - 2 : 0; ok && i < g; ++i)   // as in the loads: the last arrivals
@@ -592,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (!values) {
     // ------------------------------------------------------------------ Q features 0..511 into TMEM, one thread per row
-    const int row = tid - 256;
+    const int row = tid - 384;
     const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     int piece = 0;
     for (; w.valid(); w.next(p)) {
@@ -600,6 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = 2 * w.u + (int)side;
       const bool there = tok < p.BT;                       // else a row of zeros
       const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(there ? tok : 0) * kHeads + row) * kDqk);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * c));
       if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status,
                                                           DSA_SITE_SHARED_EMPTY)))
         break;
@@ -628,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive_cluster(cluster_addr(q_full, 0));
       ++piece;
     }
-  } else {
+  } else if (warp < 12) {
     // ------------------------------------------------------------------ O: rescaling and output; one thread per row and
     // half of the features
     const int row = (tid - 128) & 127, half = (tid - 128) >> 7;
