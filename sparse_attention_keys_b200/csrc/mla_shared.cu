@@ -22,9 +22,9 @@
 // reads the lengths.
 //
 // Score CTA: Q features 0..511 in TMEM [0, 256) (A operand, bf16 pairs), 512..575 in shared memory;
-// two score buffers in TMEM [256, 512); two staging buffers for P; K through a ring of 16 KB slots
+// two score buffers in TMEM [256, 512); three staging buffers for P; K through a ring of 16 KB slots
 // (64 keys x 128 features, this CTA's half of the tile's keys, five slots a tile).
-// Value CTA: O in all 512 TMEM columns; two P buffers; V through a ring of the same slots (64 keys x
+// Value CTA: O in all 512 TMEM columns; three P buffers; V through a ring of the same slots (64 keys x
 // 128 features: this CTA's half of the 256 features of an MMA, four slots a tile).
 #include <math.h>
 
@@ -41,18 +41,20 @@ constexpr int kHeads = 128;
 constexpr int kDqk = 576, kDv = 512;
 constexpr int kTile = 128;                         // keys per tile
 constexpr int kBlock = 16384;                      // 64 features (or keys) of 128 rows; a ring slot
-constexpr int kSlots = 8;
+constexpr int kSlots = 6;
+constexpr int kPBufs = 3;
 // the same offsets in every CTA of the cluster, so that one descriptor serves both CTAs of a pair and
 // a buffer's address in another CTA is its own address there
-constexpr int kOffP = kBlock;                      // [2][2 blocks of 64 keys]: staging, or P
-constexpr int kOffRing = kOffP + 4 * kBlock;       // [0, kBlock): Q features 512..575
-constexpr int kOffAlpha = kOffRing + kSlots * kBlock;   // [2][128] fp32
-constexpr int kOffL = kOffAlpha + 2 * 128 * 4;     // [4][128] fp32
-constexpr int kOffMax = kOffL + 4 * 128 * 4;       // [2][2][128] fp32
-constexpr int kOffBar = kOffMax + 4 * 128 * 4;
+constexpr int kOffP = kBlock;                      // [3][2 blocks of 64 keys]: staging, or P
+constexpr int kOffRing = kOffP + kPBufs * 2 * kBlock;   // [0, kBlock): Q features 512..575
+constexpr int kOffAlpha = kOffRing + kSlots * kBlock;   // [3][128] fp32
+constexpr int kOffL = kOffAlpha + kPBufs * 128 * 4;     // [4][128] fp32
+constexpr int kOffMax = kOffL + 4 * 128 * 4;            // [2][128] fp32
+constexpr int kOffSum = kOffMax + 2 * 128 * 4;          // [4][128][2] fp32
+constexpr int kOffBar = kOffSum + 4 * 128 * 8;
 constexpr int kSmem = 1024 + kOffBar + 512;
 static_assert(kSmem + 1024 <= 232448, "shared memory per CTA");
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;
 constexpr uint32_t kTmemS = 256;                   // score CTA: Q in [0, 256), scores in 2 x 128 columns
 constexpr float kLn2 = 0.69314718055994530942f;
 // The running maximum moves, and O is rescaled, only when a tile exceeds it by 2^32: P stays below
@@ -181,18 +183,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* alpha_sm = reinterpret_cast<float*>(smem + kOffAlpha);
   float* l_sm = reinterpret_cast<float*>(smem + kOffL);
   float* max_sm = reinterpret_cast<float*>(smem + kOffMax);
+  float2* sum_sm = reinterpret_cast<float2*>(smem + kOffSum);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* full = bars;                 // leader of each pair [kSlots]: both CTAs' parts of the slot have landed
   uint64_t* empty = full + kSlots;       // both of a pair [kSlots]: the MMAs that read the slot are done
   uint64_t* s_full = empty + kSlots;     // score CTAs [2]: scores ready
   uint64_t* s_free = s_full + 2;         // rank 0 [2]: both score CTAs have read the scores
-  uint64_t* p_full = s_free + 2;         // value CTAs [2]: this CTA's probabilities and factors have landed
-  uint64_t* p_ready = p_full + 2;        // rank 2 [2]: both value CTAs have them, O is rescaled
-  uint64_t* pv_done = p_ready + 2;       // all [2]: P V of the tile done
-  uint64_t* l_full = pv_done + 2;        // value CTAs [4]: the piece's sums have landed
+  uint64_t* p_full = s_free + 2;         // value CTAs [3]: this CTA's probabilities and factors have landed
+  uint64_t* p_ready = p_full + kPBufs;   // rank 2 [3]: both value CTAs have them, O is rescaled
+  uint64_t* pv_done = p_ready + kPBufs;  // all [3]: P V of the tile done
+  uint64_t* l_full = pv_done + kPBufs;   // value CTAs [4]: the piece's sums have landed
   uint64_t* q_full = l_full + 4;         // rank 0: Q of both score CTAs in place
   uint64_t* q_empty = q_full + 1;        // score CTAs: the piece's Q K^T done
   uint64_t* o_free = q_empty + 1;        // rank 2: both value CTAs have read O
+  uint64_t* m_full = o_free + 1;         // score CTAs [2][4]: to a softmax group, per quadrant: the running maximum
+  uint64_t* sum_full = m_full + 8;       // score CTAs [4][4]: to the first group: the second one's sums of a piece
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ long long scan_sh[kThreads / 32];
@@ -211,12 +216,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 16);
-      mbar_init(&p_full[i], 8);
+      mbar_init(&s_free[i], 8);
+    }
+    for (int i = 0; i < kPBufs; ++i) {
+      mbar_init(&p_full[i], 4);
       mbar_init(&p_ready[i], 16);
       mbar_init(&pv_done[i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&l_full[i], 4);
+    for (int i = 0; i < 8; ++i) mbar_init(&m_full[i], 1);
+    for (int i = 0; i < 16; ++i) mbar_init(&sum_full[i], 1);
     mbar_init(q_full, 8 + 2);
     mbar_init(q_empty, 1);
     mbar_init(o_free, 16);
@@ -276,6 +285,45 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t ring = smem_u32(smem + kOffRing);
   Walk w;
   w.start(p, (int)start_sh[0], start_sh[1], count);
+
+  // Score CTA, warps 0, 2, 3 and 9 (one per TMEM quadrant): Q features 0..511 of 32 rows into TMEM, one thread per row,
+  // once the MMAs of the piece before are done. A unit's second token may not exist: its rows are zeros.
+  auto q_rows = [&](int piece) {
+    const int row = 32 * (warp & 3) + lane;
+    const int tok = 2 * w.u + (int)side;
+    const bool there = tok < p.BT;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(there ? tok : 0) * kHeads + row) * kDqk);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * c));
+    if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status,
+                                                        DSA_SITE_SHARED_EMPTY)))
+      return false;
+    tc_fence_after();
+    const uint32_t t_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+#pragma unroll 1
+    for (int c = 0; c < 8; c += 2) {
+      uint4 v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = there ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[4 * i] = v[8 * h + i].x;
+          x[4 * i + 1] = v[8 * h + i].y;
+          x[4 * i + 2] = v[8 * h + i].z;
+          x[4 * i + 3] = v[8 * h + i].w;
+        }
+        tmem_st32(t_row + 32 * (c + h), x);
+      }
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_cluster(cluster_addr(q_full, 0));
+    return true;
+  };
 
   if (warp == 0 || warp == 2 || warp == 3) {
     // ------------------------------------------------------------------ loads
@@ -344,12 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (; ok && w.valid(); w.next(p)) {
       if (w.empty(p)) continue;
-      if (!values && mine == 0) {
-        // the last 64 features of Q
-        if (piece > 0 && !mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        if (el) {
+      if (!values) {
+        k_tile(get_tile(p, w.x, w.t0));
+        ok = ok && q_rows(piece);
+        if (ok && mine == 0 && el) {                       // the last 64 features of Q
           const uint32_t bar = cluster_addr(q_full, 0);
           arrive_expect_tx_cluster(bar, kBlock);
           pair_load_2d(smem_u32(smem), &q_map, bar, 512, (2 * w.u + (int)side) * kHeads);
@@ -359,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = w.t0; ok && t < w.t1; ++t) {
         const Tile tile = get_tile(p, w.x, t);
         if (!values) {
-          k_tile(tile);
+          if (t > w.t0) k_tile(tile);
           continue;
         }
         for (int i = 0; ok && 64 * (i >> 1) < tile.most(); ++i, advance()) {
@@ -376,7 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issue: one thread of each leader
+    // ------------------------------------------------------------------ MMA issue: one thread of each leader. The whole
+    // role runs inside elect_one(): only then does the compiler keep the operands in uniform registers,
+    // and an MMA takes its 65 cycles to issue (with a lane test, or with the warp around it, about 120)
     if (side == 0 && elect_one()) {
       int slot = 0, piece = 0;
       uint32_t ph = 0, g = 0;             // ring phase, tiles so far
@@ -428,11 +476,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const uint32_t idesc = idesc_f32acc(1, 1, 256, 256, 0, 1);
         const uint64_t p_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffP)), v_desc = sdesc_mnmajor_sw128(ring, 8192, 1024);
+        uint32_t buf = 0, pb = 0;
         for (; ok && w.valid(); w.next(p)) {
           if (w.empty(p)) continue;
           bool startedA = false, startedB = false;
           if (piece > 0 && !mbar_wait(o_free, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O)) break;
-          for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+          for (int t = w.t0; ok && t < w.t1; ++t) {
             const Tile tile = get_tile(p, w.x, t);
             // the token that sees nothing of the tile keeps its O
             const uint32_t off0 = tile.nA > 0 ? 0u : 0xffffffffu, off1 = tile.nB > 0 ? 0u : 0xffffffffu;
@@ -440,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             startedA |= tile.nA > 0;
             startedB |= tile.nB > 0;
             const int n = tile.most();
-            if (!mbar_wait(&p_ready[g & 1], (g >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) {
+            if (!mbar_wait(&p_ready[buf], pb, &abort_flag, p.status, DSA_SITE_SHARED_P)) {
               ok = false;
               break;
             }
@@ -452,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const bool part = n - kb < 64;
               if (tile.src >= 0 && part) cluster_fence();            // both CTAs' warps wrote this slot
               const uint32_t d = tmem + 256 * (i & 1);
-              const uint64_t a = p_desc + (uint64_t)(((2 * (g & 1) + (i >> 1)) * kBlock) >> 4);
+              const uint64_t a = p_desc + (uint64_t)(((2 * buf + (i >> 1)) * kBlock) >> 4);
               const uint64_t b = v_desc + (uint64_t)((slot * kBlock) >> 4);
               if ((off0 | off1) == 0 && !part) {
 #pragma unroll
@@ -464,84 +513,105 @@ __global__ void __launch_bounds__(kThreads, 1)
               pair_commit(&empty[slot], 12);
               advance();
             }
-            if (ok) pair_commit(&pv_done[g & 1], 15);
+            if (ok) pair_commit(&pv_done[buf], 15);
+            if (++buf == kPBufs) {
+              buf = 0;
+              pb ^= 1;
+            }
           }
           ++piece;
         }
       }
     }
-  } else if (!values && warp < 12) {
-    // ------------------------------------------------------------------ softmax: two threads per row, 64 keys each
-    // (one thread per row took 3500 cycles a tile, more than the tile's MMAs)
-    const int row = (tid - 128) & 127, half = (tid - 128) >> 7, quad = warp & 3;     // row: head, TMEM lane
-    const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16) + 64 * half;
+  } else if (!values) {
+    // ------------------------------------------------------------------ softmax: one thread per row, two warpgroups that
+    // take the tiles in turn. A tile takes a warpgroup about 3500 cycles, so one alone would be slower
+    // than its MMAs (2306). The running maximum passes from one to the other as soon as it is known.
+    const int row = (tid - 128) & 127, group = (tid - 128) >> 7, quad = warp & 3;    // row: head, TMEM lane
+    const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t peer = rank + 2;
-    uint32_t g = 0;
+    uint32_t g = 0, pb = 0, pph = 1;                       // tiles; P buffer and the phase of its release
     int piece = 0;
     bool ok = true;
     int32_t info_cont = -1, info_head = -1;
-    auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); };   // the two warps of these rows
     for (; ok && w.valid(); w.next(p)) {
       const int tok = 2 * w.u + (int)side;
       const bool some = !w.empty(p);
-      float m = -INFINITY, l = 0.f;                        // l: of this thread's keys
-      for (int t = w.t0; some && ok && t < w.t1; ++t, ++g) {
+      if (some && warp == 9 && !q_rows(piece)) break;
+      float m = -INFINITY, l = 0.f;                        // l: of this group's tiles, relative to m
+      for (int t = w.t0; some && ok && t < w.t1; ++t) {
+        const uint32_t buf = g & 1, ph = (g >> 1) & 1, pbuf = pb, pphase = pph;
+        const bool mine = buf == (uint32_t)group;
+        ++g;
+        if (++pb == kPBufs) {
+          pb = 0;
+          pph ^= 1;
+        }
+        if (!mine) continue;
         const Tile tile = get_tile(p, w.x, t);
         const int n = side == 0 ? tile.nA : tile.nB;
-        const uint32_t buf = g & 1, ph = (g >> 1) & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&s_full[buf], ph, &abort_flag, p.status, DSA_SITE_SHARED_S))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        uint32_t r[2][32];
+        uint32_t r[4][32];
         if (n > 0) {
-          tmem_ld32(t_row + kTmemS + buf * kTile, r[0]);
-          tmem_ld32(t_row + kTmemS + buf * kTile + 32, r[1]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_row + kTmemS + buf * kTile + 32 * c, r[c]);
           tmem_ld_wait();
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_cluster(cluster_addr(&s_free[buf], 0));
-        const uint32_t bar = cluster_addr(&p_full[buf], peer);
-        float alpha = 1.f, mm = 0.f;
+        float mx = -INFINITY;
         if (n > 0) {
           if (n < kTile) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 4; ++c)
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (64 * half + 32 * c + i >= n) r[c][i] = 0xff800000u;
+                if (32 * c + i >= n) r[c][i] = 0xff800000u;
           }
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx4[4];
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 4; ++c) {
+            mx4[c] = __uint_as_float(r[c][0]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(r[c][i]));
-          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          max_sm[(2 * buf + half) * 128 + row] = mx;
-          pair_sync();
-          mx = fmaxf(mx, max_sm[(2 * buf + (half ^ 1)) * 128 + row]) * p.scale_log2;
-          if (mx > m + kRescale) {
-            if (m != -INFINITY) alpha = exp2_approx(m - mx);
-            m = mx;
+            for (int i = 1; i < 32; ++i) mx4[c] = fmaxf(mx4[c], __uint_as_float(r[c][i]));
           }
-          mm = m == -INFINITY ? 0.f : m;                   // every score -inf: e^-inf = 0, not NaN
+          mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * p.scale_log2;
         }
-        // the staging buffer, and the value CTA's, held the tile before the last
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[buf], ph ^ 1, &abort_flag, p.status, DSA_SITE_SHARED_P))) {
+        // the maximum after the tile before (g - 2; g counts this one), from the other group
+        if (g > 1 && !__all_sync(0xffffffffu, mbar_wait(&m_full[4 * group + quad], ((g - 2) >> 1) & 1, &abort_flag, p.status,
+                                                        DSA_SITE_SHARED_S))) {
           ok = false;
           break;
         }
+        const float before = t > w.t0 ? max_sm[(buf ^ 1) * 128 + row] : -INFINITY;
+        const float now = mx > before + kRescale ? mx : before;
+        max_sm[buf * 128 + row] = now;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m_full[4 * (group ^ 1) + quad]);
+        // the staging buffer, and the value CTA's, held an earlier tile
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[pbuf], pphase, &abort_flag, p.status, DSA_SITE_SHARED_P))) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = cluster_addr(&p_full[pbuf], peer);
         if (n == 0) {
           if (lane == 0) arrive_cluster(bar);
           continue;
         }
+        const float mm = now == -INFINITY ? 0.f : now;     // every score -inf: e^-inf = 0, not NaN
+        if (now != m) {
+          l *= m == -INFINITY ? 0.f : exp2_approx(m - now);
+          m = now;
+        }
+        const uint32_t stage = smem_u32(smem + kOffP) + pbuf * 2 * kBlock + row * 128;
         float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-        uint8_t* stage = smem + kOffP + (2 * buf + half) * kBlock;
-        const uint32_t stage_row = smem_u32(stage) + row * 128;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {                      // eight keys, 16 bytes
+        for (int c = 0; c < 16; ++c) {                      // eight keys, 16 bytes
           uint32_t pk[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -550,30 +620,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum4[i] += e0 + e1;
             pk[i] = pack_bf16(e0, e1);
           }
-          st_shared_16(stage_row + ((c ^ (row & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+          st_shared_16(stage + (c >> 3) * kBlock + (((c & 7) ^ (row & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
         }
-        l = l * alpha + ((sum4[0] + sum4[1]) + (sum4[2] + sum4[3]));
-        if (half == 0) alpha_sm[buf * 128 + row] = alpha;
+        l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+        alpha_sm[pbuf * 128 + row] = now == before || before == -INFINITY ? 1.f : exp2_approx(before - now);
         fence_proxy_async_smem();
         __syncwarp();
         if (elect_one()) {
-          arrive_expect_tx_cluster(bar, half == 0 ? 4096 + 128 : 4096);
-          const uint8_t* src = stage + quad * 4096;
-          copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 4096, bar);
-          if (half == 0) {
-            const float* factors = alpha_sm + buf * 128 + 32 * quad;
-            copy_to_cluster(cluster_addr(factors, peer), smem_u32(factors), 128, bar);
+          arrive_expect_tx_cluster(bar, 2 * 4096 + 128);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t* src = smem + kOffP + (2 * pbuf + i) * kBlock + quad * 4096;
+            copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 4096, bar);
           }
+          const float* src = alpha_sm + pbuf * 128 + 32 * quad;
+          copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 128, bar);
         }
       }
       if (!ok) break;
-      if (some) {
-        // the row's sum, for the value CTA (four buffers: it may still be two pieces behind)
-        const int i = piece & 3;
-        if (half == 1) l_sm[i * 128 + row] = l;
-        pair_sync();
-        if (half == 0) {
-          l += l_sm[i * 128 + row];
+      const bool whole = w.t0 == 0 && w.t1 == w.x.tiles;
+      const int where = w.t0 == 0 ? 1 : 0;
+      if (!whole) (where ? info_head : info_cont) = w.u;
+      // the row's sum over both groups, for the value CTA too (four buffers: a reader may be two pieces behind)
+      const int i = piece & 3;
+      if (some && group == 1) {
+        sum_sm[i * 128 + row] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sum_full[4 * i + quad]);
+      }
+      if (group == 0) {
+        if (some) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&sum_full[4 * i + quad], (piece >> 2) & 1, &abort_flag, p.status,
+                                                 DSA_SITE_SHARED_S))) {
+            ok = false;
+            break;
+          }
+          const float2 other = sum_sm[i * 128 + row];
+          const float both = fmaxf(m, other.x);
+          l = (l == 0.f ? 0.f : l * exp2_approx(m - both)) + (other.y == 0.f ? 0.f : other.y * exp2_approx(other.x - both));
+          m = both;
           l_sm[i * 128 + row] = l;
           fence_proxy_async_smem();
           __syncwarp();
@@ -584,12 +669,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             copy_to_cluster(cluster_addr(src, peer), smem_u32(src), 128, bar);
           }
         }
-        ++piece;
-      }
-      const bool whole = w.t0 == 0 && w.t1 == w.x.tiles;
-      const int where = w.t0 == 0 ? 1 : 0;
-      if (!whole) (where ? info_head : info_cont) = w.u;
-      if (half == 0) {
         if (whole) {
           if (tok < p.BT && p.lse) p.lse[(int64_t)tok * kHeads + row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         } else {
@@ -597,54 +676,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<float2*>(p.part_ml + (slot * 256 + (int)side * kHeads + row) * 2) = make_float2(m, l);
         }
       }
+      piece += some;
     }
-    for (uint32_t i = g > 2 ? g - 2 : 0; ok && i < g; ++i)   // as in the loads: the last arrivals
-      if (!mbar_wait(&pv_done[i & 1], (i >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) ok = false;
+    // as in the loads: the last arrivals
+    for (uint32_t i = g > kPBufs ? g - kPBufs : 0; ok && i < g; ++i)
+      if (!mbar_wait(&pv_done[i % kPBufs], (i / kPBufs) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P)) ok = false;
     if (rank == 0 && tid == 128) {
       p.info[2 * cluster] = info_cont;
       p.info[2 * cluster + 1] = info_head;
     }
-  } else if (!values) {
-    // ------------------------------------------------------------------ Q features 0..511 into TMEM, one thread per row
-    const int row = tid - 384;
-    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    int piece = 0;
-    for (; w.valid(); w.next(p)) {
-      if (w.empty(p)) continue;
-      const int tok = 2 * w.u + (int)side;
-      const bool there = tok < p.BT;                       // else a row of zeros
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(there ? tok : 0) * kHeads + row) * kDqk);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * c));
-      if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status,
-                                                          DSA_SITE_SHARED_EMPTY)))
-        break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < 8; c += 2) {
-        uint4 v[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = there ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[32];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[4 * i] = v[8 * h + i].x;
-            x[4 * i + 1] = v[8 * h + i].y;
-            x[4 * i + 2] = v[8 * h + i].z;
-            x[4 * i + 3] = v[8 * h + i].w;
-          }
-          tmem_st32(t_row + 32 * (c + h), x);
-        }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(cluster_addr(q_full, 0));
-      ++piece;
-    }
-  } else if (warp < 12) {
+  } else {
     // ------------------------------------------------------------------ O: rescaling and output; one thread per row and
     // half of the features
     const int row = (tid - 128) & 127, half = (tid - 128) >> 7;
@@ -658,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool any = false;                                    // O of this token holds something
       for (int t = w.t0; some && ok && t < w.t1; ++t, ++g) {
         const Tile tile = get_tile(p, w.x, t);
-        const uint32_t buf = g & 1, ph = (g >> 1) & 1;
+        const uint32_t buf = g % kPBufs, ph = (g / kPBufs) & 1;
         if (!__all_sync(0xffffffffu, mbar_wait(&p_full[buf], ph, &abort_flag, p.status, DSA_SITE_SHARED_P))) {
           ok = false;
           break;
@@ -667,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float alpha = any ? alpha_sm[buf * 128 + row] : 1.f;
           if (__any_sync(0xffffffffu, alpha != 1.f)) {
             // P V of every earlier tile has to be in O first
-            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status,
+            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[(g - 1) % kPBufs], ((g - 1) / kPBufs) & 1, &abort_flag, p.status,
                                                    DSA_SITE_SHARED_O))) {
               ok = false;
               break;
@@ -695,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float l = 0.f;
       if (some) {
         const bool there = mbar_wait(&l_full[piece & 3], (piece >> 2) & 1, &abort_flag, p.status, DSA_SITE_SHARED_P) &&
-                           mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O);
+                           mbar_wait(&pv_done[(g - 1) % kPBufs], ((g - 1) / kPBufs) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O);
         if (!__all_sync(0xffffffffu, there)) {
           ok = false;
           break;
