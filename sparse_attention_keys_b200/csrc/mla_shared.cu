@@ -51,7 +51,8 @@ constexpr int kOffAlpha = kOffRing + kSlots * kBlock;   // [3][128] fp32
 constexpr int kOffL = kOffAlpha + kPBufs * 128 * 4;     // [4][128] fp32
 constexpr int kOffMax = kOffL + 4 * 128 * 4;            // [2][128] fp32
 constexpr int kOffSum = kOffMax + 2 * 128 * 4;          // [4][128][2] fp32
-constexpr int kOffBar = kOffSum + 4 * 128 * 8;
+constexpr int kOffScratch = kOffSum + 4 * 128 * 8;      // [4][32 rows][64 bytes]
+constexpr int kOffBar = kOffScratch + 4 * 2048;
 constexpr int kSmem = 1024 + kOffBar + 512;
 static_assert(kSmem + 1024 <= 232448, "shared memory per CTA");
 constexpr int kThreads = 384;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ long long scan_sh[kThreads / 32];
+  __shared__ int longest_sh[kThreads / 32];
   __shared__ long long start_sh[2];      // first unit of this cluster's range, first tile of it
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -249,7 +251,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long o = __shfl_up_sync(0xffffffffu, pre, d);
     if (lane >= d) pre += o;
   }
-  if (lane == 31) scan_sh[warp] = pre;
+  int longest = per == 1 ? (int)sum : 0;   // the longest unit (asked for only where per is 1)
+  longest = __reduce_max_sync(0xffffffffu, longest);
+  if (lane == 31) {
+    scan_sh[warp] = pre;
+    longest_sh[warp] = longest;
+  }
   if (tid == 0) start_sh[0] = start_sh[1] = 0;
   tc_fence_before();
   __syncthreads();
@@ -259,14 +266,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w == warp) base = total;
     total += scan_sh[w];
+    longest = max(longest, longest_sh[w]);
   }
   const long long excl = base + pre - sum;
-  // no more clusters than tiles: the join walks over consecutive clusters, none of them without a tile
-  const int active = (int)min((long long)clusters, total);
-  const long long share = total < (1ll << 31) ? (long long)((uint32_t)total / (uint32_t)active) : total / active;
-  const int rest = (int)(total - share * active);
-  const long long lo = cluster < active ? share * cluster + min(cluster, rest) : total;
-  const long long count = cluster < active ? share + (cluster < rest) : 0;
+  // Equal shares of whole tiles; the join walks over consecutive clusters, none of them without a tile.
+  const long long share = total < (1ll << 31) ? (long long)(((uint32_t)total + clusters - 1) / (uint32_t)clusters)
+                                              : (total + clusters - 1) / clusters;
+  long long lo = min(total, share * cluster), count = min(total - lo, share);
+  // A cut costs its two clusters about 4 tiles each (256 KB of fp32 per value CTA) and the join as much again:
+  // whole units, at most one per cluster, where the largest is not that much longer than a share
+  // (shared_b64: 72 against 67 tiles).
+  if (units <= clusters && longest <= share + 8) {
+    lo = -1;
+    if (tid == cluster) {
+      start_sh[0] = cluster;
+      start_sh[1] = 0;
+    }
+    count = cluster < units ? load_unit(p, cluster).tiles : 0;
+  }
   if (sum > 0 && lo >= excl && lo < excl + sum) {
     long long off = lo - excl;
     int u = ua;
@@ -286,36 +303,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk w;
   w.start(p, (int)start_sh[0], start_sh[1], count);
 
-  // Score CTA, warps 0, 2, 3 and 9 (one per TMEM quadrant): Q features 0..511 of 32 rows into TMEM, one thread per row,
+  // Score CTA, warps 0..3 (one per TMEM quadrant): Q features 0..511 of 32 rows into TMEM, one thread per row,
   // once the MMAs of the piece before are done. A unit's second token may not exist: its rows are zeros.
   auto q_rows = [&](int piece) {
     const int row = 32 * (warp & 3) + lane;
     const int tok = 2 * w.u + (int)side;
     const bool there = tok < p.BT;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((int64_t)(there ? tok : 0) * kHeads + row) * kDqk);
+    // The reads are coalesced, eight rows of 64 bytes (32 features) each; a TMEM lane holds a row, so the
+    // pieces turn over in 2 KB of shared memory. (Every lane reading its own row took 13000 cycles.)
+    const uint4* src =
+        reinterpret_cast<const uint4*>(p.q + ((int64_t)(there ? tok : 0) * kHeads + (row & 96) + (lane >> 2)) * kDqk) + (lane & 3);
+    const uint32_t scratch = smem_u32(smem + kOffScratch) + (warp & 3) * 2048;
+    const uint32_t put = scratch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+    const uint32_t t_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    uint4 v[4][4];
+    auto fetch = [&](int h) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + 8 * c));
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[j][i] = there ? __ldg(src + (4 * h + j) * 4 + i * 8 * (kDqk / 8)) : make_uint4(0, 0, 0, 0);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      for (int j = lane & 3; there && j < 8; j += 4) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * 8 * (kDqk / 8) + 8 * j - (lane & 3)));
+    fetch(0);
     if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status,
                                                         DSA_SITE_SHARED_EMPTY)))
       return false;
     tc_fence_after();
-    const uint32_t t_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll 1
-    for (int c = 0; c < 8; c += 2) {
-      uint4 v[16];
+    for (int h = 0; h < 4; ++h) {
+      if (h > 0) fetch(h);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = there ? __ldg(src + 8 * c + i) : make_uint4(0, 0, 0, 0);
+      for (int j = 0; j < 4; ++j) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t x[32];
+        for (int i = 0; i < 4; ++i) st_shared_16(put + i * 512, v[j][i]);
+        __syncwarp();
+        uint32_t x[16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[4 * i] = v[8 * h + i].x;
-          x[4 * i + 1] = v[8 * h + i].y;
-          x[4 * i + 2] = v[8 * h + i].z;
-          x[4 * i + 3] = v[8 * h + i].w;
+        for (int i = 0; i < 4; ++i) {
+          const uint4 y = ld_shared_16(scratch + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
+          x[4 * i] = y.x;
+          x[4 * i + 1] = y.y;
+          x[4 * i + 2] = y.z;
+          x[4 * i + 3] = y.w;
         }
-        tmem_st32(t_row + 32 * (c + h), x);
+        tmem_st16(t_row + (4 * h + j) * 16, x);
+        __syncwarp();
       }
     }
     tmem_st_wait();
@@ -422,12 +457,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issue: one thread of each leader. The whole
-    // role runs inside elect_one(): only then does the compiler keep the operands in uniform registers,
-    // and an MMA takes its 65 cycles to issue (with a lane test, or with the warp around it, about 120)
-    if (side == 0 && elect_one()) {
+    // ------------------------------------------------------------------ MMA issue: one thread of each leader. Everything the
+    // issuing loops change lives inside the elect_one() block: only then does the compiler keep the
+    // operands in uniform registers, and an MMA takes its 65 cycles to issue (otherwise about 120)
+    if (!values) {
+      const uint32_t idesc = idesc_f32acc(1, 1, 256, kTile, 0, 0);
+      const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(ring);
+      uint32_t done = 0;                  // tiles of earlier pieces
+      int piece = 0;
+      for (; w.valid(); w.next(p)) {
+        if (w.empty(p)) continue;
+        if (!q_rows(piece)) break;        // the whole warp
+        bool fine = true;
+        if (side == 0 && elect_one()) {
+          bool ok = mbar_wait(q_full, piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q);
+          tc_fence_after();
+          uint32_t g = done, slot = 5 * done % kSlots, ph = (5 * done / kSlots) & 1;
+          for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
+            const uint32_t buf = g & 1, d = tmem + kTmemS + buf * kTile;
+            if (!mbar_wait(&s_free[buf], ((g >> 1) + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_S)) ok = false;
+#pragma unroll
+            for (int f = 0; f < 9; f += 2) {
+              if (!ok || !mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_SHARED_FULL)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t b = k_desc + (uint64_t)((slot * kBlock) >> 4);
+              if (f < 8) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  pair_mma_ts(d, tmem + 32 * f + 8 * k, b + 2 * (k & 3) + (k >> 2) * (8192 >> 4), idesc, (f | k) != 0);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) pair_mma_ss(d, q_desc + 2 * k, b + 2 * k, idesc, 1);
+              }
+              pair_commit(&empty[slot], 3);
+              if (++slot == kSlots) {
+                slot = 0;
+                ph ^= 1;
+              }
+            }
+            if (ok) pair_commit(&s_full[buf], 3);
+          }
+          if (ok) pair_commit(q_empty, 3);
+          fine = ok;
+        }
+        if (!__all_sync(0xffffffffu, fine)) break;
+        done += w.t1 - w.t0;
+        ++piece;
+      }
+    } else if (side == 0 && elect_one()) {
       int slot = 0, piece = 0;
-      uint32_t ph = 0, g = 0;             // ring phase, tiles so far
+      uint32_t ph = 0;                    // ring phase
       bool ok = true;
       auto wait_full = [&]() {
         if (!mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_SHARED_FULL)) ok = false;
@@ -439,41 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ph ^= 1;
         }
       };
-      if (!values) {
-        const uint32_t idesc = idesc_f32acc(1, 1, 256, kTile, 0, 0);
-        const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(ring);
-        for (; ok && w.valid(); w.next(p)) {
-          if (w.empty(p)) continue;
-          if (!mbar_wait(q_full, piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q)) break;
-          tc_fence_after();
-          for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-            const uint32_t buf = g & 1, d = tmem + kTmemS + buf * kTile;
-            if (!mbar_wait(&s_free[buf], ((g >> 1) + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_S)) {
-              ok = false;
-              break;
-            }
-#pragma unroll
-            for (int f = 0; f < 9; f += 2) {
-              if (ok) wait_full();
-              if (!ok) break;
-              const uint64_t b = k_desc + (uint64_t)((slot * kBlock) >> 4);
-              if (f < 8) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  pair_mma_ts(d, tmem + 32 * f + 8 * k, b + 2 * (k & 3) + (k >> 2) * (8192 >> 4), idesc, (f | k) != 0);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) pair_mma_ss(d, q_desc + 2 * k, b + 2 * k, idesc, 1);
-              }
-              pair_commit(&empty[slot], 3);
-              advance();
-            }
-            if (ok) pair_commit(&s_full[buf], 3);
-          }
-          if (ok) pair_commit(q_empty, 3);
-          ++piece;
-        }
-      } else {
+      {
         const uint32_t idesc = idesc_f32acc(1, 1, 256, 256, 0, 1);
         const uint64_t p_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffP)), v_desc = sdesc_mnmajor_sw128(ring, 8192, 1024);
         uint32_t buf = 0, pb = 0;
@@ -537,7 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && w.valid(); w.next(p)) {
       const int tok = 2 * w.u + (int)side;
       const bool some = !w.empty(p);
-      if (some && warp == 9 && !q_rows(piece)) break;
       float m = -INFINITY, l = 0.f;                        // l: of this group's tiles, relative to m
       for (int t = w.t0; some && ok && t < w.t1; ++t) {
         const uint32_t buf = g & 1, ph = (g >> 1) & 1, pbuf = pb, pphase = pph;
