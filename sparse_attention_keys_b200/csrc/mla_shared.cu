@@ -174,6 +174,121 @@ __device__ __forceinline__ void load_slot(const CUtensorMap* pmap, const CUtenso
   else pair_load_4d(dst, smap, bar, 0, row, block, src);
 }
 
+// The barriers, as offsets in one array.
+enum Bar : int {
+  kFull = 0,                 // leader of each pair [kSlots]: both CTAs' parts of the slot have landed
+  kEmpty = kFull + kSlots,   // both of a pair [kSlots]: the MMAs that read the slot are done
+  kSFull = kEmpty + kSlots,  // score CTAs [2]: scores ready
+  kSFree = kSFull + 2,       // rank 0 [2]: both score CTAs have read the scores
+  kPFull = kSFree + 2,       // value CTAs [3]: this CTA's probabilities and factors have landed
+  kPReady = kPFull + kPBufs, // rank 2 [3]: both value CTAs have them, O is rescaled
+  kPvDone = kPReady + kPBufs,  // all [3]: P V of the tile done
+  kLFull = kPvDone + kPBufs, // value CTAs [4]: the piece's sums have landed
+  kQFull = kLFull + 4,       // rank 0: Q of both score CTAs in place
+  kQEmpty = kQFull + 1,      // score CTAs: the piece's Q K^T done
+  kOFree = kQEmpty + 1,      // rank 2: both value CTAs have read O
+  kMFull = kOFree + 1,       // score CTAs [2][4]: to a softmax group, per quadrant: the running maximum
+  kSumFull = kMFull + 8,     // score CTAs [4][4]: to the first group: the second one's sums of a piece
+  kBars = kSumFull + 16
+};
+static_assert(kBars * 8 <= 512, "room for the barriers");
+
+// The Q K^T of a piece, issued by one warp of rank 0 (`done` tiles came before). The loops and waits are the
+// whole warp's and every value in them the same in all lanes, only the MMAs are one thread's: then their
+// operands stay in uniform registers and an MMA takes its 65 cycles to issue. (With the loops inside the one
+// thread's branch it took about 120: 4.0 instead of 2.65 million cycles for shared_chunk.) For the same reason
+// TMEM addresses are constants: a CTA that allocates all 512 columns gets them from column 0 on.
+__device__ __forceinline__ bool issue_scores(uint8_t* smem, uint64_t* bars, uint32_t done, uint32_t tiles, uint32_t parity,
+                                             int* abort_flag, int* status) {
+  const uint32_t idesc = idesc_f32acc(1, 1, 256, kTile, 0, 0);
+  const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffRing));
+  done = __shfl_sync(0xffffffffu, done, 0);
+  tiles = __shfl_sync(0xffffffffu, tiles, 0);
+  auto wait = [&](uint64_t* bar, uint32_t phase, int site) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag, status, site)) != 0;
+  };
+  if (!wait(bars + kQFull, parity, DSA_SITE_SHARED_Q)) return false;
+  tc_fence_after();
+  uint32_t slot = 5 * done % kSlots, ph = (5 * done / kSlots) & 1;
+  for (uint32_t g = done; g < done + tiles; ++g) {
+    const uint32_t buf = g & 1, d = kTmemS + buf * kTile;
+    if (!wait(bars + kSFree + buf, ((g >> 1) + 1) & 1, DSA_SITE_SHARED_S)) return false;
+#pragma unroll
+    for (int f = 0; f < 9; f += 2) {
+      if (!wait(bars + kFull + slot, ph, DSA_SITE_SHARED_FULL)) return false;
+      tc_fence_after();
+      const uint64_t b = k_desc + (uint64_t)((slot * kBlock) >> 4);
+      if (elect_one()) {
+        if (f < 8) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            pair_mma_ts(d, 32 * f + 8 * k, b + 2 * (k & 3) + (k >> 2) * (8192 >> 4), idesc, (f | k) != 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) pair_mma_ss(d, q_desc + 2 * k, b + 2 * k, idesc, 1);
+        }
+        pair_commit(bars + kEmpty + slot, 3);
+        if (f == 8) pair_commit(bars + kSFull + buf, 3);
+      }
+      __syncwarp();
+      if (++slot == kSlots) {
+        slot = 0;
+        ph ^= 1;
+      }
+    }
+  }
+  if (elect_one()) pair_commit(bars + kQEmpty, 3);
+  __syncwarp();
+  return true;
+}
+
+// Features 0..511 of 32 rows of Q (q: the first one) into TMEM at t_row, a row per lane. The reads are
+// coalesced, eight rows of 64 bytes each, the next 128 features in flight while the last turn over in
+// 2 KB of shared memory. (Every lane reading its own row took 13000 cycles.)
+__device__ __forceinline__ void q_features(const uint16_t* q, bool there, uint32_t scratch, uint32_t t_row) {
+  const int lane = threadIdx.x & 31;
+  const uint4* src = reinterpret_cast<const uint4*>(q + (lane >> 2) * kDqk) + (lane & 3);
+  const uint32_t put = scratch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+  const uint32_t get = scratch + lane * 64;
+  const uint32_t turn = (lane >> 1) & 3;
+  uint4 va[4][4], vb[4][4];
+  auto fetch = [&](uint4 (&v)[4][4], int h) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[j][i] = there ? __ldg(src + (4 * h + j) * 4 + i * 8 * (kDqk / 8)) : make_uint4(0, 0, 0, 0);
+  };
+  auto store = [&](const uint4 (&v)[4][4], int h) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st_shared_16(put + i * 512, v[j][i]);
+      __syncwarp();
+      uint32_t x[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 y = ld_shared_16(get + ((i ^ turn) << 4));
+        x[4 * i] = y.x;
+        x[4 * i + 1] = y.y;
+        x[4 * i + 2] = y.z;
+        x[4 * i + 3] = y.w;
+      }
+      tmem_st16(t_row + (4 * h + j) * 16, x);
+      __syncwarp();
+    }
+  };
+  fetch(va, 0);
+#pragma unroll 1
+  for (int h = 0; h < 4; h += 2) {
+    fetch(vb, h + 1);
+    store(va, h);
+    if (h == 0) fetch(va, 2);
+    store(vb, h + 1);
+  }
+  tmem_st_wait();
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -186,19 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* max_sm = reinterpret_cast<float*>(smem + kOffMax);
   float2* sum_sm = reinterpret_cast<float2*>(smem + kOffSum);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint64_t* full = bars;                 // leader of each pair [kSlots]: both CTAs' parts of the slot have landed
-  uint64_t* empty = full + kSlots;       // both of a pair [kSlots]: the MMAs that read the slot are done
-  uint64_t* s_full = empty + kSlots;     // score CTAs [2]: scores ready
-  uint64_t* s_free = s_full + 2;         // rank 0 [2]: both score CTAs have read the scores
-  uint64_t* p_full = s_free + 2;         // value CTAs [3]: this CTA's probabilities and factors have landed
-  uint64_t* p_ready = p_full + kPBufs;   // rank 2 [3]: both value CTAs have them, O is rescaled
-  uint64_t* pv_done = p_ready + kPBufs;  // all [3]: P V of the tile done
-  uint64_t* l_full = pv_done + kPBufs;   // value CTAs [4]: the piece's sums have landed
-  uint64_t* q_full = l_full + 4;         // rank 0: Q of both score CTAs in place
-  uint64_t* q_empty = q_full + 1;        // score CTAs: the piece's Q K^T done
-  uint64_t* o_free = q_empty + 1;        // rank 2: both value CTAs have read O
-  uint64_t* m_full = o_free + 1;         // score CTAs [2][4]: to a softmax group, per quadrant: the running maximum
-  uint64_t* sum_full = m_full + 8;       // score CTAs [4][4]: to the first group: the second one's sums of a piece
+  uint64_t *full = bars + kFull, *empty = bars + kEmpty, *s_full = bars + kSFull, *s_free = bars + kSFree;
+  uint64_t *p_full = bars + kPFull, *p_ready = bars + kPReady, *pv_done = bars + kPvDone, *l_full = bars + kLFull;
+  uint64_t *q_full = bars + kQFull, *q_empty = bars + kQEmpty, *o_free = bars + kOFree, *m_full = bars + kMFull;
+  uint64_t* sum_full = bars + kSumFull;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ long long scan_sh[kThreads / 32];
@@ -273,16 +379,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long share = total < (1ll << 31) ? (long long)(((uint32_t)total + clusters - 1) / (uint32_t)clusters)
                                               : (total + clusters - 1) / clusters;
   long long lo = min(total, share * cluster), count = min(total - lo, share);
-  // A cut costs its two clusters about 4 tiles each (256 KB of fp32 per value CTA) and the join as much again:
-  // whole units, at most one per cluster, where the largest is not that much longer than a share
-  // (shared_b64: 72 against 67 tiles).
-  if (units <= clusters && longest <= share + 8) {
-    lo = -1;
-    if (tid == cluster) {
-      start_sh[0] = cluster;
-      start_sh[1] = 0;
+  // A cut inside a share costs its cluster another Q, another pipeline fill and 256 KB of fp32 per value CTA, about 8
+  // tiles: where there are no more units than clusters, every unit gets the same number of clusters and an equal
+  // share in each, if the longest share is not that much longer (shared_b64: 72 against 67 tiles, no cuts at
+  // all; shared_b8: eight clusters a unit).
+  const int group = units <= clusters ? (int)((uint32_t)clusters / (uint32_t)units) : 1;
+  const int part = (int)((uint32_t)(longest + group - 1) / (uint32_t)group);
+  if (units <= clusters && part <= share + 8) {
+    lo = -1;                             // found here, not by the search below
+    const int u = (int)((uint32_t)cluster / (uint32_t)group), first = (cluster - u * group) * part;
+    count = u < units ? max(0, min(part, load_unit(p, u).tiles - first)) : 0;
+    if (tid == 0) {
+      start_sh[0] = u;
+      start_sh[1] = first;
     }
-    count = cluster < units ? load_unit(p, cluster).tiles : 0;
   }
   if (sum > 0 && lo >= excl && lo < excl + sum) {
     long long off = lo - excl;
@@ -303,57 +413,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk w;
   w.start(p, (int)start_sh[0], start_sh[1], count);
 
-  // Score CTA, warps 0..3 (one per TMEM quadrant): Q features 0..511 of 32 rows into TMEM, one thread per row,
-  // once the MMAs of the piece before are done. A unit's second token may not exist: its rows are zeros.
+  // Score CTA, warps 0..3 (one per TMEM quadrant): the piece's Q into TMEM, once the MMAs of the piece before are done.
   auto q_rows = [&](int piece) {
-    const int row = 32 * (warp & 3) + lane;
-    const int tok = 2 * w.u + (int)side;
-    const bool there = tok < p.BT;
-    // The reads are coalesced, eight rows of 64 bytes (32 features) each; a TMEM lane holds a row, so the
-    // pieces turn over in 2 KB of shared memory. (Every lane reading its own row took 13000 cycles.)
-    const uint4* src =
-        reinterpret_cast<const uint4*>(p.q + ((int64_t)(there ? tok : 0) * kHeads + (row & 96) + (lane >> 2)) * kDqk) + (lane & 3);
-    const uint32_t scratch = smem_u32(smem + kOffScratch) + (warp & 3) * 2048;
-    const uint32_t put = scratch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-    const uint32_t t_row = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    uint4 v[4][4];
-    auto fetch = [&](int h) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[j][i] = there ? __ldg(src + (4 * h + j) * 4 + i * 8 * (kDqk / 8)) : make_uint4(0, 0, 0, 0);
-    };
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      for (int j = lane & 3; there && j < 8; j += 4) asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i * 8 * (kDqk / 8) + 8 * j - (lane & 3)));
-    fetch(0);
     if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status,
                                                         DSA_SITE_SHARED_EMPTY)))
       return false;
-    tc_fence_after();
-#pragma unroll 1
-    for (int h = 0; h < 4; ++h) {
-      if (h > 0) fetch(h);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st_shared_16(put + i * 512, v[j][i]);
-        __syncwarp();
-        uint32_t x[16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 y = ld_shared_16(scratch + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
-          x[4 * i] = y.x;
-          x[4 * i + 1] = y.y;
-          x[4 * i + 2] = y.z;
-          x[4 * i + 3] = y.w;
-        }
-        tmem_st16(t_row + (4 * h + j) * 16, x);
-        __syncwarp();
-      }
+    if (warp == 0 && elect_one()) {        // the last 64 features go to shared memory
+      const uint32_t bar = cluster_addr(q_full, 0);
+      arrive_expect_tx_cluster(bar, kBlock);
+      pair_load_2d(smem_u32(smem), &q_map, bar, 512, (2 * w.u + (int)side) * kHeads);
     }
-    tmem_st_wait();
+    __syncwarp();
+    tc_fence_after();
+    const int tok = 2 * w.u + (int)side;
+    const bool there = tok < p.BT;         // a unit's second token may not exist: its rows are zeros
+    q_features(p.q + ((int64_t)(there ? tok : 0) * kHeads + 32 * warp) * kDqk, there,
+               smem_u32(smem + kOffScratch) + warp * 2048, tmem + ((uint32_t)(32 * warp) << 16));
     tc_fence_before();
     __syncwarp();
     if (lane == 0) arrive_cluster(cluster_addr(q_full, 0));
@@ -430,11 +505,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!values) {
         k_tile(get_tile(p, w.x, w.t0));
         ok = ok && q_rows(piece);
-        if (ok && mine == 0 && el) {                       // the last 64 features of Q
-          const uint32_t bar = cluster_addr(q_full, 0);
-          arrive_expect_tx_cluster(bar, kBlock);
-          pair_load_2d(smem_u32(smem), &q_map, bar, 512, (2 * w.u + (int)side) * kHeads);
-        }
       }
       ++piece;
       for (int t = w.t0; ok && t < w.t1; ++t) {
@@ -457,118 +527,81 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_EMPTY);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issue: one thread of each leader. Everything the
-    // issuing loops change lives inside the elect_one() block: only then does the compiler keep the
-    // operands in uniform registers, and an MMA takes its 65 cycles to issue (otherwise about 120)
+    // ------------------------------------------------------------------ MMA issue: one thread of each leader
     if (!values) {
-      const uint32_t idesc = idesc_f32acc(1, 1, 256, kTile, 0, 0);
-      const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(ring);
       uint32_t done = 0;                  // tiles of earlier pieces
       int piece = 0;
       for (; w.valid(); w.next(p)) {
         if (w.empty(p)) continue;
         if (!q_rows(piece)) break;        // the whole warp
-        bool fine = true;
-        if (side == 0 && elect_one()) {
-          bool ok = mbar_wait(q_full, piece & 1, &abort_flag, p.status, DSA_SITE_SHARED_Q);
-          tc_fence_after();
-          uint32_t g = done, slot = 5 * done % kSlots, ph = (5 * done / kSlots) & 1;
-          for (int t = w.t0; ok && t < w.t1; ++t, ++g) {
-            const uint32_t buf = g & 1, d = tmem + kTmemS + buf * kTile;
-            if (!mbar_wait(&s_free[buf], ((g >> 1) + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_S)) ok = false;
-#pragma unroll
-            for (int f = 0; f < 9; f += 2) {
-              if (!ok || !mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_SHARED_FULL)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint64_t b = k_desc + (uint64_t)((slot * kBlock) >> 4);
-              if (f < 8) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  pair_mma_ts(d, tmem + 32 * f + 8 * k, b + 2 * (k & 3) + (k >> 2) * (8192 >> 4), idesc, (f | k) != 0);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) pair_mma_ss(d, q_desc + 2 * k, b + 2 * k, idesc, 1);
-              }
-              pair_commit(&empty[slot], 3);
-              if (++slot == kSlots) {
-                slot = 0;
-                ph ^= 1;
-              }
-            }
-            if (ok) pair_commit(&s_full[buf], 3);
-          }
-          if (ok) pair_commit(q_empty, 3);
-          fine = ok;
-        }
+        const bool fine = side != 0 || issue_scores(smem, bars, done, (uint32_t)(w.t1 - w.t0), piece & 1, &abort_flag, p.status);
         if (!__all_sync(0xffffffffu, fine)) break;
         done += w.t1 - w.t0;
         ++piece;
       }
-    } else if (side == 0 && elect_one()) {
-      int slot = 0, piece = 0;
-      uint32_t ph = 0;                    // ring phase
+    } else if (side == 0) {
+      const uint32_t idesc = idesc_f32acc(1, 1, 256, 256, 0, 1);
+      const uint64_t p_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffP)), v_desc = sdesc_mnmajor_sw128(ring, 8192, 1024);
+      auto wait = [&](uint64_t* bar, uint32_t phase, int site) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, phase, &abort_flag, p.status, site)) != 0;
+      };
+      uint32_t slot = 0, ph = 0, buf = 0, pb = 0;          // ring slot and phase, P buffer and phase
+      int piece = 0;
       bool ok = true;
-      auto wait_full = [&]() {
-        if (!mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_SHARED_FULL)) ok = false;
-        tc_fence_after();
-      };
-      auto advance = [&]() {
-        if (++slot == kSlots) {
-          slot = 0;
-          ph ^= 1;
-        }
-      };
-      {
-        const uint32_t idesc = idesc_f32acc(1, 1, 256, 256, 0, 1);
-        const uint64_t p_desc = sdesc_kmajor_sw128(smem_u32(smem + kOffP)), v_desc = sdesc_mnmajor_sw128(ring, 8192, 1024);
-        uint32_t buf = 0, pb = 0;
-        for (; ok && w.valid(); w.next(p)) {
-          if (w.empty(p)) continue;
-          bool startedA = false, startedB = false;
-          if (piece > 0 && !mbar_wait(o_free, (piece + 1) & 1, &abort_flag, p.status, DSA_SITE_SHARED_O)) break;
-          for (int t = w.t0; ok && t < w.t1; ++t) {
-            const Tile tile = get_tile(p, w.x, t);
-            // the token that sees nothing of the tile keeps its O
-            const uint32_t off0 = tile.nA > 0 ? 0u : 0xffffffffu, off1 = tile.nB > 0 ? 0u : 0xffffffffu;
-            const bool acc = (tile.nA > 0 && startedA) || (tile.nB > 0 && startedB);
-            startedA |= tile.nA > 0;
-            startedB |= tile.nB > 0;
-            const int n = tile.most();
-            if (!mbar_wait(&p_ready[buf], pb, &abort_flag, p.status, DSA_SITE_SHARED_P)) {
+      for (; ok && w.valid(); w.next(p)) {
+        if (w.empty(p)) continue;
+        if (piece > 0 && !wait(o_free, (piece + 1) & 1, DSA_SITE_SHARED_O)) break;
+        bool startedA = false, startedB = false;
+        for (int t = w.t0; ok && t < w.t1; ++t) {
+          const Tile tile = get_tile(p, w.x, t);
+          // the token that sees nothing of the tile keeps its O
+          const uint32_t off0 = tile.nA > 0 ? 0u : 0xffffffffu, off1 = tile.nB > 0 ? 0u : 0xffffffffu;
+          const bool acc = (tile.nA > 0 && startedA) || (tile.nB > 0 && startedB);
+          startedA |= tile.nA > 0;
+          startedB |= tile.nB > 0;
+          const int n = tile.most();
+          if (!wait(&p_ready[buf], pb, DSA_SITE_SHARED_P)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const bool plain = acc && (off0 | off1) == 0 && n == kTile;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {                    // 64 keys x 256 features each
+            const int kb = 64 * (i >> 1);
+            if (kb >= n) break;
+            if (!wait(&full[slot], ph, DSA_SITE_SHARED_FULL)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            for (int i = 0; ok && 64 * (i >> 1) < n; ++i) {
-              const int kb = 64 * (i >> 1);
-              wait_full();
-              if (!ok) break;
-              const bool part = n - kb < 64;
-              if (tile.src >= 0 && part) cluster_fence();            // both CTAs' warps wrote this slot
-              const uint32_t d = tmem + 256 * (i & 1);
-              const uint64_t a = p_desc + (uint64_t)(((2 * buf + (i >> 1)) * kBlock) >> 4);
-              const uint64_t b = v_desc + (uint64_t)((slot * kBlock) >> 4);
-              if ((off0 | off1) == 0 && !part) {
+            if (tile.src >= 0 && n - kb < 64) cluster_fence();       // both CTAs' warps wrote this slot
+            const uint64_t a = p_desc + (uint64_t)((2 * buf + (i >> 1)) * (kBlock >> 4));
+            const uint64_t b = v_desc + (uint64_t)(slot * (kBlock >> 4));
+            if (elect_one()) {
+              if (plain) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) pair_mma_ss(d, a + 2 * k, b + 128 * k, idesc, acc || kb + k > 0);
+                for (int k = 0; k < 4; ++k) pair_mma_ss(256 * (i & 1), a + 2 * k, b + 128 * k, idesc, 1);
               } else {
                 for (int k = 0; k < 4 && kb + 16 * k < n; ++k)
-                  pair_mma_ss_masked(d, a + 2 * k, b + 128 * k, idesc, off0, off1, acc || kb + k > 0);
+                  pair_mma_ss_masked(256 * (i & 1), a + 2 * k, b + 128 * k, idesc, off0, off1, acc || kb + k > 0);
               }
               pair_commit(&empty[slot], 12);
-              advance();
             }
-            if (ok) pair_commit(&pv_done[buf], 15);
-            if (++buf == kPBufs) {
-              buf = 0;
-              pb ^= 1;
+            __syncwarp();
+            if (++slot == kSlots) {
+              slot = 0;
+              ph ^= 1;
             }
           }
-          ++piece;
+          if (ok && elect_one()) pair_commit(&pv_done[buf], 15);
+          __syncwarp();
+          if (++buf == kPBufs) {
+            buf = 0;
+            pb ^= 1;
+          }
         }
+        ++piece;
       }
     }
   } else if (!values) {
@@ -844,53 +877,83 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) pair_tmem_dealloc(tmem, 512);
 }
 
-// Joins the pieces of units that were cut: block (c, y) takes 32 rows x 64 features of the unit whose
-// first piece is the last one of cluster c; the pieces that follow are the first ones of the next.
+// Joins the pieces of units that were cut. A unit's first piece is the last one of some cluster c, the others
+// are the first ones of the clusters behind it. The blocks take (cut unit, 32 rows x 64 features) in turn: most
+// clusters head no unit, and a block for each of them cost more than the joining (20 us for shared_b8).
 __global__ void __launch_bounds__(256) mla_shared_join_kernel(const SharedParams p, int clusters) {
   extern __shared__ float2 ml_sh[];      // [pieces][32 rows]: maximum, sum
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
-  const int unit = __ldcg(p.info + 2 * c + 1);
-  if (unit < 0) return;
-  const int row = (blockIdx.y >> 3) * 32 + lane, col = (blockIdx.y & 7) * 64 + 8 * warp;
-  const int tok = 2 * unit + (row >> 7), head = row & 127;
-  if (tok >= p.BT) return;               // the same for the whole block
-  int n = 1;                             // pieces
-  for (int q = c + 1; q < clusters; q += 32) {
-    const uint32_t other = __ballot_sync(0xffffffffu, q + lane >= clusters || __ldcg(p.info + 2 * (q + lane)) != unit);
-    n += other ? __ffs(other) - 1 : 32;
-    if (other) break;
-  }
-  auto slot_of = [&](int i) { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
-  for (int i = warp; i < n; i += 8)
-    ml_sh[i * 32 + lane] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(i) * 256 + row);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, ml_sh[i * 32 + lane].x);
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  const float4* src = reinterpret_cast<const float4*>(p.part_o) + (int64_t)(col / 4) * 256 + row;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = ml_sh[i * 32 + lane];
-    // a piece without a visible key has sum 0 and no maximum
-    const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - m);
-    l += ml.y * f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float4 v = __ldcg(src + slot_of(i) * (128 * 256) + j * 256);
-      acc[j].x = fmaf(v.x, f, acc[j].x);
-      acc[j].y = fmaf(v.y, f, acc[j].y);
-      acc[j].z = fmaf(v.z, f, acc[j].z);
-      acc[j].w = fmaf(v.w, f, acc[j].w);
+  for (int work = blockIdx.x;; work += gridDim.x) {
+    int c = -1, heads = 0;
+    for (int q = 0; q < clusters && c < 0; q += 32) {
+      const uint32_t mask = __ballot_sync(0xffffffffu, q + lane < clusters && __ldcg(p.info + 2 * (q + lane) + 1) >= 0);
+      const int k = (work >> 6) - heads;
+      if (k < __popc(mask)) c = q + (int)__fns(mask, 0, k + 1);
+      heads += __popc(mask);
     }
+    if (c < 0) return;
+    const int unit = __ldcg(p.info + 2 * c + 1), part = work & 63;
+    const int row = (part >> 3) * 32 + lane, col = (part & 7) * 64 + 8 * warp;
+    const int tok = 2 * unit + (row >> 7), head = row & 127;
+    if (tok >= p.BT) continue;             // the same for the whole block
+    int n = 1;                             // pieces
+    for (int q = c + 1; q < clusters; q += 32) {
+      const uint32_t other = __ballot_sync(0xffffffffu, q + lane >= clusters || __ldcg(p.info + 2 * (q + lane)) != unit);
+      n += other ? __ffs(other) - 1 : 32;
+      if (other) break;
+    }
+    auto slot_of = [&](int i) { return i == 0 ? (int64_t)c * 2 + 1 : (int64_t)(c + i) * 2; };
+    const float4* src = reinterpret_cast<const float4*>(p.part_o) + (int64_t)(col / 4) * 256 + row;
+    // the first four pieces' values travel together with the maxima and sums
+    float4 v[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) v[i][j] = __ldcg(src + slot_of(min(i, n - 1)) * (128 * 256) + j * 256);
+    for (int i = warp; i < n; i += 8)
+      ml_sh[i * 32 + lane] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of(i) * 256 + row);
+    __syncthreads();
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, ml_sh[i * 32 + lane].x);
+    float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int i0 = 0; i0 < n; i0 += 4) {
+      float4 next[4][2];
+      if (i0 + 4 < n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) next[i][j] = __ldcg(src + slot_of(min(i0 + 4 + i, n - 1)) * (128 * 256) + j * 256);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i0 + i >= n) break;
+        const float2 ml = ml_sh[(i0 + i) * 32 + lane];
+        // a piece without a visible key has sum 0 and no maximum
+        const float f = ml.y == 0.f ? 0.f : exp2_approx(ml.x - m);
+        l += ml.y * f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          acc[j].x = fmaf(v[i][j].x, f, acc[j].x);
+          acc[j].y = fmaf(v[i][j].y, f, acc[j].y);
+          acc[j].z = fmaf(v[i][j].z, f, acc[j].z);
+          acc[j].w = fmaf(v[i][j].w, f, acc[j].w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) v[i][j] = next[i][j];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t out_row = (int64_t)tok * kHeads + head;
+    *reinterpret_cast<uint4*>(p.out + out_row * kDv + col) =
+        make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
+                   pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
+    if (col == 0 && p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    __syncthreads();                     // ml_sh is written again
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t out_row = (int64_t)tok * kHeads + head;
-  *reinterpret_cast<uint4*>(p.out + out_row * kDv + col) =
-      make_uint4(pack_bf16(acc[0].x * inv, acc[0].y * inv), pack_bf16(acc[0].z * inv, acc[0].w * inv),
-                 pack_bf16(acc[1].x * inv, acc[1].y * inv), pack_bf16(acc[1].z * inv, acc[1].w * inv));
-  if (col == 0 && p.lse) p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 namespace {
@@ -988,7 +1051,7 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
   }
   int rc = dsa_host::launch_clusters(mla_shared_kernel, 4, (unsigned)clusters, kThreads, kSmem, stream, q_map, pm, sm, p);
   if (rc != DSA_OK) return rc;
-  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)clusters, 64), dim3(256), (size_t)clusters * 32 * 8, stream,
+  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)(2 * dsa_host::device_sm_count())), dim3(256), (size_t)clusters * 32 * 8, stream,
                           p, clusters);
 }
 
