@@ -187,7 +187,9 @@ enum Bar : int {
   kQFull = kLFull + 4,       // rank 0: Q of both score CTAs in place
   kQEmpty = kQFull + 1,      // score CTAs: the piece's Q K^T done
   kOFree = kQEmpty + 1,      // rank 2: both value CTAs have read O
-  kMFull = kOFree + 1,       // score CTAs [2][4]: to a softmax group, per quadrant: the running maximum
+  kQStage = kOFree + 1,      // score CTAs: most of the first Q in shared memory
+  kQHelp = kQStage + 1,      // rank 0: it is in both score CTAs' TMEM
+  kMFull = kQHelp + 1,       // score CTAs [2][4]: to a softmax group, per quadrant: the running maximum
   kSumFull = kMFull + 8,     // score CTAs [4][4]: to the first group: the second one's sums of a piece
   kBars = kSumFull + 16
 };
@@ -208,6 +210,7 @@ __device__ __forceinline__ bool issue_scores(uint8_t* smem, uint64_t* bars, uint
     return __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag, status, site)) != 0;
   };
   if (!wait(bars + kQFull, parity, DSA_SITE_SHARED_Q)) return false;
+  if (done == 0 && !wait(bars + kQHelp, 0, DSA_SITE_SHARED_Q)) return false;
   tc_fence_after();
   uint32_t slot = 5 * done % kSlots, ph = (5 * done / kSlots) & 1;
   for (uint32_t g = done; g < done + tiles; ++g) {
@@ -242,24 +245,21 @@ __device__ __forceinline__ bool issue_scores(uint8_t* smem, uint64_t* bars, uint
   return true;
 }
 
-// Features 0..511 of 32 rows of Q (q: the first one) into TMEM at t_row, a row per lane. The reads are
-// coalesced, eight rows of 64 bytes each, the next 128 features in flight while the last turn over in
-// 2 KB of shared memory. (Every lane reading its own row took 13000 cycles.)
-__device__ __forceinline__ void q_features(const uint16_t* q, bool there, uint32_t scratch, uint32_t t_row) {
+// Features [128 from, 512) of 32 rows of Q (q: the first one) into TMEM at t_row, a row per lane. The reads
+// are coalesced, eight rows of 64 bytes each, and turn over in 2 KB of shared memory. (Every lane
+// reading its own row took 13000 cycles for the 512 features.)
+__device__ __forceinline__ void q_features(const uint16_t* q, bool there, uint32_t scratch, uint32_t t_row, int from) {
   const int lane = threadIdx.x & 31;
   const uint4* src = reinterpret_cast<const uint4*>(q + (lane >> 2) * kDqk) + (lane & 3);
   const uint32_t put = scratch + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
-  const uint32_t get = scratch + lane * 64;
-  const uint32_t turn = (lane >> 1) & 3;
-  uint4 va[4][4], vb[4][4];
-  auto fetch = [&](uint4 (&v)[4][4], int h) {
+#pragma unroll 1
+  for (int h = from; h < 4; ++h) {
+    uint4 v[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         v[j][i] = there ? __ldg(src + (4 * h + j) * 4 + i * 8 * (kDqk / 8)) : make_uint4(0, 0, 0, 0);
-  };
-  auto store = [&](const uint4 (&v)[4][4], int h) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
 #pragma unroll
@@ -268,7 +268,7 @@ __device__ __forceinline__ void q_features(const uint16_t* q, bool there, uint32
       uint32_t x[16];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 y = ld_shared_16(get + ((i ^ turn) << 4));
+        const uint4 y = ld_shared_16(scratch + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4));
         x[4 * i] = y.x;
         x[4 * i + 1] = y.y;
         x[4 * i + 2] = y.z;
@@ -277,14 +277,6 @@ __device__ __forceinline__ void q_features(const uint16_t* q, bool there, uint32
       tmem_st16(t_row + (4 * h + j) * 16, x);
       __syncwarp();
     }
-  };
-  fetch(va, 0);
-#pragma unroll 1
-  for (int h = 0; h < 4; h += 2) {
-    fetch(vb, h + 1);
-    store(va, h);
-    if (h == 0) fetch(va, 2);
-    store(vb, h + 1);
   }
   tmem_st_wait();
 }
@@ -304,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *full = bars + kFull, *empty = bars + kEmpty, *s_full = bars + kSFull, *s_free = bars + kSFree;
   uint64_t *p_full = bars + kPFull, *p_ready = bars + kPReady, *pv_done = bars + kPvDone, *l_full = bars + kLFull;
   uint64_t *q_full = bars + kQFull, *q_empty = bars + kQEmpty, *o_free = bars + kOFree, *m_full = bars + kMFull;
-  uint64_t* sum_full = bars + kSumFull;
+  uint64_t *sum_full = bars + kSumFull, *q_stage = bars + kQStage, *q_help = bars + kQHelp;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
   __shared__ long long scan_sh[kThreads / 32];
@@ -337,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_full, 8 + 2);
     mbar_init(q_empty, 1);
     mbar_init(o_free, 16);
+    mbar_init(q_stage, 1);
+    mbar_init(q_help, 16);
     fence_barrier_init();
   }
   if (warp == 2) pair_tmem_alloc(&tmem_base_sh, 512);
@@ -413,22 +407,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk w;
   w.start(p, (int)start_sh[0], start_sh[1], count);
 
-  // Score CTA, warps 0..3 (one per TMEM quadrant): the piece's Q into TMEM, once the MMAs of the piece before are done.
+  // Score CTA: Q of a piece, once the MMAs of the piece before are done. Features 512..575 stay in shared memory, the
+  // others go into TMEM, by warps 0..3 (one per TMEM quadrant). The first piece has no pipeline to overlap with:
+  // there TMA brings features 0..383 into the still unused P buffers, and the softmax warps take them from there.
+  auto q_tma = [&](int piece) {
+    const int row = (2 * w.u + (int)side) * kHeads;
+    const uint32_t bar = cluster_addr(q_full, 0);
+    arrive_expect_tx_cluster(bar, kBlock);
+    pair_load_2d(smem_u32(smem), &q_map, bar, 512, row);
+    if (piece > 0) return;
+    mbar_arrive_expect_tx(q_stage, 6 * kBlock);
+    for (int i = 0; i < 6; ++i) tma_load_2d(smem + kOffP + i * kBlock, &q_map, q_stage, 64 * i, row);
+  };
   auto q_rows = [&](int piece) {
     if (piece > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (piece + 1) & 1, &abort_flag, p.status,
                                                         DSA_SITE_SHARED_EMPTY)))
       return false;
-    if (warp == 0 && elect_one()) {        // the last 64 features go to shared memory
-      const uint32_t bar = cluster_addr(q_full, 0);
-      arrive_expect_tx_cluster(bar, kBlock);
-      pair_load_2d(smem_u32(smem), &q_map, bar, 512, (2 * w.u + (int)side) * kHeads);
-    }
+    if (piece > 0 && warp == 0 && elect_one()) q_tma(piece);
     __syncwarp();
     tc_fence_after();
     const int tok = 2 * w.u + (int)side;
     const bool there = tok < p.BT;         // a unit's second token may not exist: its rows are zeros
     q_features(p.q + ((int64_t)(there ? tok : 0) * kHeads + 32 * warp) * kDqk, there,
-               smem_u32(smem + kOffScratch) + warp * 2048, tmem + ((uint32_t)(32 * warp) << 16));
+               smem_u32(smem + kOffScratch) + warp * 2048, tmem + ((uint32_t)(32 * warp) << 16), piece > 0 ? 0 : 3);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) arrive_cluster(cluster_addr(q_full, 0));
@@ -503,6 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && w.valid(); w.next(p)) {
       if (w.empty(p)) continue;
       if (!values) {
+        if (piece == 0 && mine == 0 && el) q_tma(0);
+        __syncwarp();
         k_tile(get_tile(p, w.x, w.t0));
         ok = ok && q_rows(piece);
       }
@@ -618,6 +621,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && w.valid(); w.next(p)) {
       const int tok = 2 * w.u + (int)side;
       const bool some = !w.empty(p);
+      if (some && piece == 0) {                            // three blocks of 64 features of the first Q
+        if (!__all_sync(0xffffffffu, mbar_wait(q_stage, 0, &abort_flag, p.status, DSA_SITE_SHARED_Q))) break;
+#pragma unroll 1
+        for (int f = 3 * group; f < 3 * group + 3; ++f) {
+          uint32_t x[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 y = ld_shared_16(smem_u32(smem + kOffP) + f * kBlock + row * 128 + ((c ^ (row & 7)) << 4));
+            x[4 * c] = y.x;
+            x[4 * c + 1] = y.y;
+            x[4 * c + 2] = y.z;
+            x[4 * c + 3] = y.w;
+          }
+          tmem_st32(t_row + 32 * f, x);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(cluster_addr(q_help, 0));
+      }
       float m = -INFINITY, l = 0.f;                        // l: of this group's tiles, relative to m
       for (int t = w.t0; some && ok && t < w.t1; ++t) {
         const uint32_t buf = g & 1, ph = (g >> 1) & 1, pbuf = pb, pphase = pph;
