@@ -38,6 +38,13 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ uint2 ld_cluster_2(const void* p, uint32_t rank) {
+  uint32_t a;
+  uint2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -57,7 +64,6 @@ struct EvictParams {
   const int32_t* kv_len;
   int S_max, keep, recent, sinks;
   int C;                   // CTAs per sequence
-  int cached;              // the rows of a CTA fit into shared memory
   float* acc_out;
   int32_t* pos_out;
   int32_t* len_out;
@@ -69,10 +75,12 @@ struct EvictParams {
   float* k_scale;
 };
 
+// CACHED: the rows of a CTA fit into shared memory.
+template <bool CACHED>
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictParams p) {
   extern __shared__ __align__(16) uint32_t rows_sm[];        // [per][2]: weight bits, position
-  __shared__ uint32_t hist[2][kBins];                        // ordinary and protected rows
-  __shared__ uint32_t cnt_sm[4];                             // this CTA's counts, read by the others
+  __shared__ __align__(16) uint32_t hist[2][kBins];                        // ordinary and protected rows
+  __shared__ uint32_t cnt_sm[8];                             // this CTA's words that the others read (kNewest ...)
   __shared__ uint32_t warp_sm[kWarps];
   __shared__ uint32_t found_sm[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -113,15 +121,19 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     return;
   }
 
-  // Shared-memory rows are not written again, so any thread may read any row after the barrier.
-  auto weight = [&](int r) { return weight_key(p.cached ? __uint_as_float(rows_sm[2 * (r - r0)]) : acc[r]); };
-  auto position = [&](int r) { return p.cached ? (int)rows_sm[2 * (r - r0) + 1] : pos[r]; };
-
+  enum { kNewest, kSafe, kTies, kHoles, kMovers };            // words of cnt_sm
+  // word `slot` of every CTA before this one, of every one behind it, and of all, summed
+  auto gather = [&](int slot, uint32_t& before, uint32_t& behind) {
+    const uint32_t v = lane < p.C ? ld_cluster(&cnt_sm[slot], (uint32_t)lane) : 0u;
+    before = __reduce_add_sync(0xffffffffu, lane < (int)rank ? v : 0u);
+    behind = __reduce_add_sync(0xffffffffu, lane > (int)rank ? v : 0u);
+    return __reduce_add_sync(0xffffffffu, v);
+  };
   for (int i = tid; i < 2 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
   int newest = INT32_MIN;
   for (int r = r0 + tid; r < r1; r += kThreads) {
     const int ps = pos[r];
-    if (p.cached) *reinterpret_cast<uint2*>(rows_sm + 2 * (r - r0)) = make_uint2(__float_as_uint(acc[r]), (uint32_t)ps);
+    if (CACHED) *reinterpret_cast<uint2*>(rows_sm + 2 * (r - r0)) = make_uint2(__float_as_uint(acc[r]), (uint32_t)ps);
     newest = max(newest, ps);
   }
 #pragma unroll
@@ -132,28 +144,37 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     newest = (int)warp_sm[lane];
 #pragma unroll
     for (int d = 16; d; d >>= 1) newest = max(newest, __shfl_xor_sync(0xffffffffu, newest, d));
-    if (lane == 0) cnt_sm[0] = (uint32_t)newest;
+    if (lane == 0) {
+      cnt_sm[kNewest] = (uint32_t)newest;
+      cnt_sm[kSafe] = 0;
+    }
   }
   sync_all();
-  newest = INT32_MIN;
-  for (int c = 0; c < p.C; ++c) newest = max(newest, (int)ld_cluster(&cnt_sm[0], (uint32_t)c));
-  const int64_t recent_from = (int64_t)newest - p.recent;     // positions above it are protected
-  auto is_safe = [&](int r) {
-    const int ps = position(r);
-    return (int64_t)ps > recent_from || ps < p.sinks;
+  newest = __reduce_max_sync(0xffffffffu, lane < p.C ? (int)ld_cluster(&cnt_sm[kNewest], (uint32_t)lane) : INT32_MIN);
+  // positions above `recent_from` are protected (all of them, if that lies below the range)
+  const int64_t from = (int64_t)newest - p.recent;
+  const int recent_from = (int)max(from, (int64_t)INT32_MIN);
+  auto protects = [&](int ps) { return ps > recent_from || ps < p.sinks || from < INT32_MIN; };
+  // A row's key and class; shared memory holds (weight, position) until the next loop, then these.
+  auto row_of = [&](int r) {
+    return CACHED ? *reinterpret_cast<const uint2*>(rows_sm + 2 * (r - r0))
+                  : make_uint2(weight_key(acc[r]), protects(pos[r]) ? 1u : 0u);
   };
 
   // first digit, for both classes
-  for (int r = r0 + tid; r < r1; r += kThreads) atomicAdd(&hist[is_safe(r) ? 1 : 0][weight(r) >> 21], 1u);
+  uint32_t safe = 0;
+  for (int r = r0 + tid; r < r1; r += kThreads) {
+    const uint2 row = CACHED ? *reinterpret_cast<const uint2*>(rows_sm + 2 * (r - r0))
+                               : make_uint2(__float_as_uint(acc[r]), (uint32_t)pos[r]);
+    const uint32_t key = weight_key(__uint_as_float(row.x));
+    const bool yes = protects((int)row.y);
+    if (CACHED) *reinterpret_cast<uint2*>(rows_sm + 2 * (r - r0)) = make_uint2(key, yes ? 1u : 0u);
+    safe += yes;
+    atomicAdd(&hist[yes ? 1 : 0][key >> 21], 1u);
+  }
+  safe = __reduce_add_sync(0xffffffffu, safe);
+  if (lane == 0 && safe) atomicAdd(&cnt_sm[kSafe], safe);
   sync_all();
-  // cluster-wide histogram of one class, two bins per thread, and its total
-  auto merged = [&](int cls, uint32_t& h0, uint32_t& h1) {
-    h0 = h1 = 0;
-    for (int c = 0; c < p.C; ++c) {
-      h0 += ld_cluster(&hist[cls][2 * tid], (uint32_t)c);
-      h1 += ld_cluster(&hist[cls][2 * tid + 1], (uint32_t)c);
-    }
-  };
   // exclusive sum over the block's threads of v, and the total
   auto block_scan = [&](uint32_t v, uint32_t& total) {
     uint32_t s = v;
@@ -175,12 +196,26 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     const uint32_t base = __shfl_sync(0xffffffffu, ws, warp ? warp - 1 : 0);
     return (warp ? base : 0u) + s - v;
   };
-  // the bin in which the want-th largest key lies, and how many keys lie in higher bins
-  auto find_bin = [&](int cls, uint32_t want, uint32_t& bin, uint32_t& above) {
-    uint32_t h0, h1, total;
-    merged(cls, h0, h1);
+  // The bin of histogram `which` in which the want-th largest key lies; `want` becomes its rank among the
+  // bin's keys. Every CTA adds up all histograms for itself, two bins a thread: that costs one cluster
+  // barrier a digit (sharing the bins out moves less, but took two more barriers and twice the time).
+  auto find_bin = [&](int which, uint32_t& want) {
+    uint32_t h0 = 0, h1 = 0, total;
+    if (p.C == 1) {
+      h0 = hist[which][2 * tid];
+      h1 = hist[which][2 * tid + 1];
+    } else {
+      uint2 h[kMaxCluster];
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) h[c] = c < p.C ? ld_cluster_2(&hist[which][2 * tid], (uint32_t)c) : make_uint2(0, 0);
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        h0 += h[c].x;
+        h1 += h[c].y;
+      }
+    }
     const uint32_t before = block_scan(h0 + h1, total);       // keys in lower bins
-    const uint32_t up1 = total - before - h0 - h1, up0 = up1 + h1;
+    const uint32_t up1 = total - before - h0 - h1, up0 = up1 + h1;     // keys in bins above
     if (want > up1 && want <= up1 + h1) {
       found_sm[0] = 2 * tid + 1;
       found_sm[1] = up1;
@@ -189,101 +224,125 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
       found_sm[1] = up0;
     }
     __syncthreads();
-    bin = found_sm[0];
-    above = found_sm[1];
+    want -= found_sm[1];
+    return found_sm[0];
   };
-  uint32_t safe_total;
-  {
-    uint32_t h0, h1;
-    merged(1, h0, h1);
-    block_scan(h0 + h1, safe_total);
-  }
+  uint32_t unused0, unused1;
+  const uint32_t safe_total = gather(kSafe, unused0, unused1);
   // the class that the border runs through, and how many of it are kept
-  const int cls = safe_total >= (uint32_t)p.keep ? 1 : 0;
+  const uint32_t cls = safe_total >= (uint32_t)p.keep ? 1 : 0;
   uint32_t want = cls ? (uint32_t)p.keep : (uint32_t)p.keep - safe_total;
-  uint32_t bin, above, prefix;
-  find_bin(cls, want, bin, above);
-  prefix = bin << 21;
-  want -= above;
-  // second and third digit, over the rows of the class that share the prefix
+  uint32_t prefix = find_bin((int)cls, want) << 21;
+  // Second and third digit, over the rows of the class that share the prefix. The histogram of the other class was
+  // for this CTA alone, and when the third digit takes the first one's again, every CTA has passed a barrier since.
   for (int digit = 1; digit <= 2; ++digit) {
-    const int shift = digit == 1 ? 10 : 0;
+    const int shift = digit == 1 ? 10 : 0, which = (int)(digit == 1 ? cls ^ 1u : cls);
     const uint32_t mask = digit == 1 ? 0xffe00000u : 0xfffffc00u;
-    sync_all();                                            // every CTA has read the histograms
-    hist[0][2 * tid] = hist[0][2 * tid + 1] = 0;
+    hist[which][2 * tid] = hist[which][2 * tid + 1] = 0;
     __syncthreads();
     for (int r = r0 + tid; r < r1; r += kThreads) {
-      const uint32_t k = weight(r);
-      if ((k & mask) == prefix && is_safe(r) == (cls != 0)) atomicAdd(&hist[0][(k >> shift) & (digit == 1 ? 2047u : 1023u)], 1u);
+      const uint2 row = row_of(r);
+      if ((row.x & mask) == prefix && row.y == cls)
+        atomicAdd(&hist[which][(row.x >> shift) & (digit == 1 ? 2047u : 1023u)], 1u);
     }
     sync_all();
-    find_bin(0, want, bin, above);
-    prefix |= bin << shift;
-    want -= above;
+    prefix |= find_bin(which, want) << shift;
   }
   // The border key is `prefix`; `want` rows of the class on it are kept, the lowest ones.
   // 0: given up, 1: kept, 2: kept if among the first `want` on the border
   auto judge = [&](int r) {
-    const bool safe = is_safe(r);
-    if (safe != (cls != 0)) return safe ? 1 : 0;
-    const uint32_t k = weight(r);
-    return k > prefix ? 1 : (k == prefix ? 2 : 0);
+    const uint2 row = row_of(r);
+    return row.y != cls ? (int)row.y : (row.x > prefix ? 1 : (row.x == prefix ? 2 : 0));
   };
   // rows on the border in this warp's run, then before it in the sequence
   const int w0 = min(r1, r0 + warp * per_warp), w1 = min(r1, w0 + per_warp);
   auto exclusive = [&](uint32_t mine, int slot) {             // over the cluster's warps, row order
-    uint32_t total;
+    uint32_t total, before, behind;
     const uint32_t base = block_scan(lane == 0 ? mine : 0u, total);
     if (tid == 0) cnt_sm[slot] = total;
     sync_all();
-    uint32_t before = 0;
-    for (uint32_t c = 0; c < rank; ++c) before += ld_cluster(&cnt_sm[slot], c);
+    gather(slot, before, behind);
     return before + __shfl_sync(0xffffffffu, base, 0);
   };
-  uint32_t ties = 0;
-  for (int r = w0 + lane; r - lane < w1; r += 32)
-    ties += __popc(__ballot_sync(0xffffffffu, r < w1 && judge(r) == 2));
-  const uint32_t ties_before = exclusive(ties, 1);
+  // two bits a row keep the judgement of the first 16 groups of a warp's run
+  uint32_t codes = 0, ties = 0;
+  auto code = [&](int it, int r) { return it < 16 ? (int)((codes >> (2 * it)) & 3u) : (r < w1 ? judge(r) : 0); };
+  for (int r = w0 + lane, it = 0; r - lane < w1; r += 32, ++it) {
+    const int j = r < w1 ? judge(r) : 0;
+    if (it < 16) codes |= (uint32_t)j << (2 * it);
+    ties += __popc(__ballot_sync(0xffffffffu, j == 2));
+  }
+  const uint32_t ties_before = exclusive(ties, kTies);
   // holes (given up, below the budget) and movers (kept, behind it): counted, then listed in row order
   const uint32_t lower = (1u << lane) - 1u;
-  auto walk = [&](auto&& visit) {
+  uint32_t holes = 0, movers = 0;
+  {
     uint32_t t = ties_before;
-    for (int r = w0 + lane; r - lane < w1; r += 32) {
-      const int j = r < w1 ? judge(r) : 0;
+    for (int r = w0 + lane, it = 0; r - lane < w1; r += 32, ++it) {
+      const int j = code(it, r);
+      const uint32_t eq = __ballot_sync(0xffffffffu, j == 2);
+      const bool kept = j == 1 || (j == 2 && t + __popc(eq & lower) < want);
+      t += __popc(eq);
+      holes += __popc(__ballot_sync(0xffffffffu, r < w1 && !kept && r < p.keep));
+      movers += __popc(__ballot_sync(0xffffffffu, kept && r >= p.keep));
+    }
+  }
+  // both in one barrier: a CTA's counts are at most its rows
+  uint32_t total, behind;
+  const uint32_t hole_base = block_scan(lane == 0 ? holes : 0u, total);
+  if (tid == 0) cnt_sm[kHoles] = total;
+  const uint32_t mover_base = block_scan(lane == 0 ? movers : 0u, total);
+  if (tid == 0) cnt_sm[kMovers] = total;
+  sync_all();
+  const uint32_t all_holes = gather(kHoles, holes, behind);
+  gather(kMovers, movers, behind);
+  holes += __shfl_sync(0xffffffffu, hole_base, 0);
+  movers += __shfl_sync(0xffffffffu, mover_base, 0);
+  // the state of rows that stay is read four groups ahead of the walk that needs it
+  float a4[4];
+  int p4[4];
+  auto fetch = [&](int r) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = r + 32 * k;
+      if (at < w1 && at < p.keep) {
+        if (copy_acc) a4[k] = acc[at];
+        if (copy_pos) p4[k] = pos[at];
+      }
+    }
+  };
+  uint32_t t = ties_before;
+  for (int r4 = w0 + lane, it4 = 0; r4 - lane < w1; r4 += 128, it4 += 4) {
+    fetch(r4);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r4 + 32 * k;
+      if (r - lane >= w1) break;
+      const int j = code(it4 + k, r);
       const uint32_t eq = __ballot_sync(0xffffffffu, j == 2);
       const bool kept = j == 1 || (j == 2 && t + __popc(eq & lower) < want);
       t += __popc(eq);
       const bool hole = r < w1 && !kept && r < p.keep, mover = kept && r >= p.keep;
-      visit(r, kept, hole, mover, __ballot_sync(0xffffffffu, hole), __ballot_sync(0xffffffffu, mover));
+      const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
+      if (hole) moves[1 + p.L + holes + __popc(hb & lower)] = r;
+      if (mover) moves[1 + movers + __popc(mb & lower)] = r;
+      if (kept && r < p.keep) {
+        if (copy_acc) acc_out[r] = a4[k];
+        if (copy_pos) pos_out[r] = p4[k];
+        if (src) src[r] = r;
+      }
+      holes += __popc(hb);
+      movers += __popc(mb);
     }
-  };
-  uint32_t holes = 0, movers = 0;
-  walk([&](int, bool, bool, bool, uint32_t hb, uint32_t mb) {
-    holes += __popc(hb);
-    movers += __popc(mb);
-  });
-  holes = exclusive(holes, 2);
-  movers = exclusive(movers, 3);
-  walk([&](int r, bool kept, bool hole, bool mover, uint32_t hb, uint32_t mb) {
-    if (hole) moves[1 + p.L + holes + __popc(hb & lower)] = r;
-    if (mover) moves[1 + movers + __popc(mb & lower)] = r;
-    if (kept && r < p.keep) {
-      if (copy_acc) acc_out[r] = acc[r];
-      if (copy_pos) pos_out[r] = pos[r];
-      if (src) src[r] = r;
-    }
-    holes += __popc(hb);
-    movers += __popc(mb);
-  });
+  }
   if (rank == 0 && tid == 0) {
     p.len_out[b] = p.keep;
-    uint32_t total = 0;                                        // as many holes as movers
-    for (int c = 0; c < p.C; ++c) total += ld_cluster(&cnt_sm[2], (uint32_t)c);
-    moves[0] = (int)total;
+    moves[0] = (int)all_holes;                                 // as many holes as movers
   }
-  sync_all();                                              // no CTA leaves while another reads it
+  sync_all();                                                  // no CTA leaves while another reads it
 }
 
+// A warp moves two rows at a time: 2.3 KB in flight per warp.
 __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p) {
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
@@ -291,32 +350,44 @@ __global__ void __launch_bounds__(256) evict_move_kernel(const EvictParams p) {
   const int32_t* moves = p.moves + (int64_t)b * (1 + 2 * p.L);
   const int count = moves[0];
   const int64_t base = (int64_t)b * p.S_max;
-  for (int i = blockIdx.x * 8 + warp; i < count; i += gridDim.x * 8) {
-    const int64_t from = base + moves[1 + i], to = base + moves[1 + p.L + i];
-    uint4 v0, v1, v2;
-    uint32_t c = 0;
-    if (p.kv) {
-      const uint4* s = reinterpret_cast<const uint4*>(p.kv + from * 1152);
-      v0 = s[lane];
-      v1 = s[lane + 32];
-      if (lane < 8) v2 = s[lane + 64];
+  for (int i = 2 * (blockIdx.x * 8 + warp); i < count; i += 2 * (int)gridDim.x * 8) {
+    int64_t from[2], to[2];
+    const bool two = i + 1 < count;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      from[k] = base + moves[1 + min(i + k, count - 1)];
+      to[k] = base + moves[1 + p.L + min(i + k, count - 1)];
     }
-    if (p.k8) c = reinterpret_cast<const uint32_t*>(p.k8 + from * 128)[lane];
-    if (lane == 0) {
-      const float a = p.acc[from];
-      const int32_t ps = p.pos[from];
-      p.acc_out[to] = a;
-      p.pos_out[to] = ps;
-      if (p.k_scale) p.k_scale[to] = p.k_scale[from];
-      if (p.src) p.src[(int64_t)b * p.keep + (to - base)] = (int32_t)(from - base);
+    uint4 v[2][3];
+    uint32_t c[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (p.kv) {
+        const uint4* s = reinterpret_cast<const uint4*>(p.kv + from[k] * 1152);
+        v[k][0] = s[lane];
+        v[k][1] = s[lane + 32];
+        if (lane < 8) v[k][2] = s[lane + 64];
+      }
+      if (p.k8) c[k] = reinterpret_cast<const uint32_t*>(p.k8 + from[k] * 128)[lane];
     }
-    if (p.kv) {
-      uint4* d = reinterpret_cast<uint4*>(p.kv + to * 1152);
-      d[lane] = v0;
-      d[lane + 32] = v1;
-      if (lane < 8) d[lane + 64] = v2;
+    if (lane < (two ? 2 : 1)) {
+      const int64_t f = lane ? from[1] : from[0], t = lane ? to[1] : to[0];
+      p.acc_out[t] = p.acc[f];
+      p.pos_out[t] = p.pos[f];
+      if (p.k_scale) p.k_scale[t] = p.k_scale[f];
+      if (p.src) p.src[(int64_t)b * p.keep + (t - base)] = (int32_t)(f - base);
     }
-    if (p.k8) reinterpret_cast<uint32_t*>(p.k8 + to * 128)[lane] = c;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (k == 1 && !two) break;
+      if (p.kv) {
+        uint4* d = reinterpret_cast<uint4*>(p.kv + to[k] * 1152);
+        d[lane] = v[k][0];
+        d[lane + 32] = v[k][1];
+        if (lane < 8) d[lane + 64] = v[k][2];
+      }
+      if (p.k8) reinterpret_cast<uint32_t*>(p.k8 + to[k] * 128)[lane] = c[k];
+    }
   }
 }
 
@@ -348,15 +419,16 @@ int launch_cache_evict(const float* acc, const int32_t* pos, const int32_t* kv_l
   p.k_scale = k_scale;
   // CTAs per sequence: enough that each takes at most 4096 rows, as far as one wave of SMs goes
   int C = 1;
+  // (clusters of 16, which are not portable, were slower for one sequence of 131072: their barriers cost more)
   while (C < kMaxCluster && (int64_t)C * 4096 < S_max && (int64_t)2 * C * B <= dsa_host::device_sm_count()) C *= 2;
   while (C < kMaxCluster && (int64_t)C * kCachedRows < S_max) C *= 2;
   p.C = C;
   const int64_t per_warp = (((int64_t)S_max + C * kWarps - 1) / (C * kWarps) + 31) / 32 * 32;
-  p.cached = per_warp * kWarps <= kCachedRows;
-  const size_t smem = p.cached ? (size_t)per_warp * kWarps * 8 : 0;
+  const bool cached = per_warp * kWarps <= kCachedRows;
+  const size_t smem = cached ? (size_t)per_warp * kWarps * 8 : 0;
   static uint64_t seen[dsa_host::kMaxSetupDevices];
   if (dsa_host::needs_setup(seen, nullptr)) {
-    if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCachedRows * 8) != cudaSuccess)
+    if (cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCachedRows * 8) != cudaSuccess)
       return DSA_ERR_CUDA;
     dsa_host::mark_setup(seen);
   }
@@ -374,7 +446,8 @@ int launch_cache_evict(const float* acc, const int32_t* pos, const int32_t* kv_l
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, evict_select_kernel, p) != cudaSuccess) return DSA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, cached ? evict_select_kernel<true> : evict_select_kernel<false>, p) != cudaSuccess)
+    return DSA_ERR_CUDA;
   if (p.L == 0) return DSA_OK;                               // the budget holds every row: no moves
   const int blocks = std::max(1, std::min((p.L + 7) / 8, std::max(1, 8 * dsa_host::device_sm_count() / B)));
   return dsa_host::launch(evict_move_kernel, dim3((unsigned)blocks, (unsigned)B), dim3(256), 0, stream, p);
