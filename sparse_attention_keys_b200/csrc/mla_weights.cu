@@ -13,8 +13,8 @@
 // take an SM's share of it 6300 cycles.
 //
 // Selected rows are gathered by four warps with 16-byte cp.async into the swizzled operand layout,
-// 128 bytes of each row per block; the whole rows of the next tile are hinted into L2 one tile
-// ahead, so that DRAM sees 1152-byte requests.
+// 128 bytes of each row per block. (Hinting whole rows into L2 a tile ahead was slower, 46.5 against
+// 43.5 us for 64 queries of 2048 rows; so was hinting the next dense tile, 55 against 50 us.)
 #include <math.h>
 
 #include <algorithm>
@@ -270,15 +270,9 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
         if (row >= p.S_max) set_status(p.status, DSA_ERR_DEVICE_BOUNDS);
         return row < p.S_max ? row : -1;
       };
-      auto hint = [&](int row) {
-        if (row >= 0)
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(kv + (int64_t)row * kDqk), "r"(kDqk * 2) : "memory");
-      };
       int row = row_of(r.t0);
-      hint(row);
       for (int t = r.t0; ok && t < r.t1; ++t) {
         const int next = row_of(t + 1);
-        hint(next);
         for (int f = 0; f < 9; ++f) {
           if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY))) {
             ok = false;
@@ -318,8 +312,9 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
       for (int t = r.t0; ok && t < r.t1; ++t, ++g) {
         const int u = t * kTile + key;
         bool take = u < r.keys;
+        int row = u;
         if (SELECTED && take) {
-          const int row = __ldg(p.idx + r.tok * p.k + u);
+          row = __ldg(p.idx + r.tok * p.k + u);
           take = row >= 0 && row < p.S_max;
         }
         if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[g % kAccs], (g / kAccs) & 1, &abort_flag, p.status,
@@ -354,7 +349,8 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
         if (u < r.keys) {
           const float sum = take ? (s4[0] + s4[1]) + (s4[2] + s4[3]) : 0.f;
           p.w[r.tok * p.ld + u] = sum;
-          if (!SELECTED && p.T == 1 && p.acc_out) p.acc_out[r.tok * p.S_max + u] = p.acc[r.tok * p.S_max + u] + sum;
+          // one query per sequence: no other weight meets this row's
+          if (take && p.T == 1 && p.acc_out) p.acc_out[r.tok * p.S_max + row] = p.acc[r.tok * p.S_max + row] + sum;
         }
       }
     }
@@ -408,7 +404,17 @@ __global__ void __launch_bounds__(256) mla_weights_sum_kernel(const WeightsParam
   }
 }
 
-// Selected: acc_out = acc + the weights of the queries in their order; a block holds kRange positions of
+// Selected, one query per sequence: what nobody selected, ahead of the kernel that adds the rest.
+__global__ void __launch_bounds__(256) mla_weights_copy_kernel(const float4* acc, float4* acc_out, int64_t n) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t stride = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n / 4; i += stride) acc_out[i] = acc[i];
+  if (blockIdx.x == 0 && threadIdx.x < n % 4)
+    reinterpret_cast<float*>(acc_out)[n - 1 - threadIdx.x] = reinterpret_cast<const float*>(acc)[n - 1 - threadIdx.x];
+}
+
+// Selected, several queries per sequence: acc_out = acc + their weights, in their order; a block holds kRange positions of
 // one sequence in shared memory. Positions of one query are distinct, so no two threads meet.
 constexpr int kRange = 4096;
 __global__ void __launch_bounds__(1024) mla_weights_scatter_kernel(const WeightsParams p) {
@@ -454,12 +460,19 @@ int launch_weights(const uint16_t* q, const WeightsParams& p, int64_t B, cudaStr
       return DSA_ERR_CUDA;
     dsa_host::mark_setup(seen);
   }
+  if (SELECTED && p.T == 1 && p.acc_out && p.acc_out != p.acc) {
+    const int64_t n = B * p.S_max;
+    const int rc = dsa_host::launch(mla_weights_copy_kernel, dim3((unsigned)std::min<int64_t>((n / 4 + 255) / 256 + 1, 1024)),
+                                    dim3(256), 0, stream, reinterpret_cast<const float4*>(p.acc),
+                                    reinterpret_cast<float4*>(p.acc_out), n);
+    if (rc != DSA_OK) return rc;
+  }
   const int64_t tiles = p.BT * (((SELECTED ? p.k : p.S_max) + kTile - 1) / kTile);
   const unsigned grid = (unsigned)std::min<int64_t>(dsa_host::device_sm_count(), tiles);
   const int rc = dsa_host::launch(mla_weights_kernel<SELECTED>, dim3(grid), dim3(SELECTED ? 384 : 256), kSmem, stream, q_map,
                                   k_map, p);
   if (rc != DSA_OK) return rc;
-  if (!SELECTED && p.T == 1) return DSA_OK;
+  if (p.T == 1) return DSA_OK;
   if (!SELECTED)
     return dsa_host::launch(mla_weights_sum_kernel, dim3((unsigned)((p.S_max + 31) / 32), (unsigned)B), dim3(256), 0, stream, p);
   if (!p.acc_out) return DSA_OK;
