@@ -7,10 +7,15 @@
 // The scores are computed transposed, S^T = K Q^T, so that a TMEM lane holds one key and the 128
 // columns its heads: the sum over the heads stays inside a thread. One CTA per SM takes an equal
 // share of all (query, 128-key tile) pairs; the query (128 x 576, 144 KB) stays in shared memory while
-// 16 KB blocks of keys (128 keys x 64 features) pass through a ring of five. Per tile 36 MMAs of
-// 128 x 128 x 16 (65 cycles each, 2340) into one of four 128-column accumulators, and 128 x 128
-// exponentials (1024 cycles of MUFU). For one query per sequence HBM is the bound: 147 KB per tile
-// take an SM's share of it 6300 cycles.
+// 16 KB blocks of keys (128 keys x 64 features) pass through a ring of five. Per tile: 36 MMAs of
+// 128 x 128 x 16 (65 cycles each, 2340) and 128 x 128 exponentials (1024 cycles of MUFU). For one query
+// per sequence HBM is the bound: 147 KB a tile take an SM's share of it 6300 cycles.
+//
+// A tile's contraction is cut into four parts of 128, 128, 128 and 192 features, each with an accumulator
+// of 128 columns of its own, that are added in registers. The exponential turns an absolute error of the score
+// into a relative one of the weight, and the tensor core's rounding of the running fp32 sum, 36 times over
+// 576 features, was what the weights' error came from: 6.7e-6 of them with one accumulator, 1.7e-6 with four
+// (fp32 matrix products leave 2e-6). It costs 5% of the time.
 //
 // Selected rows are gathered by four warps with 16-byte cp.async into the swizzled operand layout,
 // 128 bytes of each row per block. (Hinting whole rows into L2 a tile ahead was slower, 46.5 against
@@ -31,11 +36,12 @@ constexpr int kBlock = 128 * 128;                  // 16 KB: 64 features of 128 
 constexpr int kSlots = 5;
 constexpr int kOffRing = 9 * kBlock;
 constexpr int kOffBar = kOffRing + kSlots * kBlock;
-constexpr int kOffLse = kOffBar + 256;             // 2 x 128 fp32
-constexpr int kOffScan = kOffLse + 2 * 128 * 4;    // set-up words
-constexpr int kSmem = 1024 + kOffScan + 256;
+constexpr int kOffLse = kOffBar + 256;             // [2][128] fp32
+constexpr int kOffSum = kOffLse + 2 * 128 * 4;     // [2][128] fp32
+constexpr int kOffScan = kOffSum + 2 * 128 * 4;    // set-up words
+constexpr int kSmem = kOffScan + 256;
 static_assert(kSmem <= 232448, "shared memory per CTA");
-constexpr int kAccs = 4;                           // accumulators of 128 columns
+constexpr int kParts = 4;                          // parts of a contraction, an accumulator of 128 columns each
 constexpr int kGatherWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -103,20 +109,25 @@ struct Runs {
 }  // namespace
 
 template <bool SELECTED>
-__global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
+__global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
     mla_weights_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                        const WeightsParams p) {
-  constexpr int kThreads = SELECTED ? 384 : 256;
+  constexpr int kThreads = SELECTED ? 512 : 384;
+  // Parts handed over at a time: two where the MMAs are the bound (250 dense queries over 4100 rows: 103 us, and
+  // 111 one by one), one where the gather is (64 queries of 2048 rows: 43.5 us, and 46 by twos).
+  constexpr int kJoint = SELECTED ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint8_t* smem = smem_raw;              // 1024-byte aligned: the kernel has no other shared memory
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* full = bars;                 // [kSlots] keys landed
   uint64_t* empty = full + kSlots;       // [kSlots] their MMAs are done
-  uint64_t* acc_full = empty + kSlots;   // [kAccs] scores ready
-  uint64_t* acc_empty = acc_full + kAccs;  // [kAccs] scores read
-  uint64_t* q_full = acc_empty + kAccs;
+  uint64_t* acc_full = empty + kSlots;   // [kParts / kJoint] parts of the scores ready
+  uint64_t* acc_empty = acc_full + kParts;  // [kParts / kJoint] they are read
+  uint64_t* q_full = acc_empty + kParts;
   uint64_t* q_empty = q_full + 1;        // the run's MMAs are done
+  uint64_t* sum_full = q_empty + 1;      // [4] the second half of the heads is summed, per quadrant
   float* lse_sh = reinterpret_cast<float*>(smem + kOffLse);
+  float* sum_sh = reinterpret_cast<float*>(smem + kOffSum);
   long long* scan_sh = reinterpret_cast<long long*>(smem + kOffScan);       // [kThreads / 32]
   long long* start_sh = scan_sh + 16;                                       // first query, tile of it
   uint32_t& tmem_base_sh = *reinterpret_cast<uint32_t*>(start_sh + 2);
@@ -129,10 +140,11 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
       mbar_init(&full[s], SELECTED ? kGatherWarps * 32 : 1);
       mbar_init(&empty[s], 1);
     }
-    for (int i = 0; i < kAccs; ++i) {
+    for (int i = 0; i < kParts; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 4);
+      mbar_init(&acc_empty[i], 8);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&sum_full[i], 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     fence_barrier_init();
@@ -213,7 +225,7 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issue
+    // ------------------------------------------------------------------ MMA issue, one thread
     if (elect_one()) {
       const uint32_t idesc = idesc_f32acc(1, 1, 128, kHeads, 0, 0);
       const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(ring);
@@ -223,41 +235,39 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
       for (; ok && r.left > 0; r.next(p), ++run) {
         if (!mbar_wait(q_full, run & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_Q)) break;
         tc_fence_after();
-        for (int t = r.t0; ok && t < r.t1; ++t, ++g) {
-          if (!mbar_wait(&acc_empty[g % kAccs], ((g / kAccs) + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem + (g % kAccs) * kHeads;
-#pragma unroll 1
+        const int tiles = r.t1 - r.t0;
+        for (int t = 0; ok && t < tiles; ++t, ++g) {
+#pragma unroll
           for (int f = 0; f < 9; ++f) {
-            if (!mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL)) {
+            const int part = f < 8 ? f >> 1 : kParts - 1;
+            const bool first = (f & 1) == 0 && f < 8;        // of its part
+            if (!ok || (first && part % kJoint == 0 && !mbar_wait(&acc_empty[part / kJoint], (g + 1) & 1, &abort_flag, p.status,
+                                                                  DSA_SITE_WEIGHTS_ACC)) ||
+                !mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL)) {
               ok = false;
               break;
             }
-            if (SELECTED) fence_proxy_async_smem();      // cp.async writes -> MMA reads
+            if (SELECTED) fence_proxy_async_smem();
             tc_fence_after();
-            const uint64_t a = k_desc + (uint64_t)((slot * kBlock) >> 4), b = q_desc + (uint64_t)((f * kBlock) >> 4);
+            const uint64_t a = k_desc + (uint64_t)(slot * (kBlock >> 4)), b = q_desc + (uint64_t)(f * (kBlock >> 4));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss(d, a + 2 * k, b + 2 * k, idesc, (f | k) != 0);
+            for (int k = 0; k < 4; ++k) mma_f16_ss(part * kHeads, a + 2 * k, b + 2 * k, idesc, k > 0 || !first);
             mma_commit(&empty[slot]);
+            if (f == 8 || ((f & 1) != 0 && f < 7 && part % kJoint == kJoint - 1)) mma_commit(&acc_full[part / kJoint]);
             if (++slot == kSlots) {
               slot = 0;
               ph ^= 1;
             }
           }
-          if (ok) mma_commit(&acc_full[g % kAccs]);
         }
         if (ok) mma_commit(q_empty);
       }
-      // the last arrivals have to reach this CTA before it leaves
       if (ok && run > 0) mbar_wait(q_empty, (run + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // ------------------------------------------------------------------ gather (selected rows)
     // warp v copies rows 32 v .. 32 v + 31 of the tile: lane i holds the row number of row 32 v + i
-    const int v = warp - 8;
+    const int v = warp - 12;
     int slot = 0;
     uint32_t ph = 1;
     bool ok = true;
@@ -299,16 +309,20 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
     }
     cp_async_wait_all();
   } else if (warp >= 4) {
-    // ------------------------------------------------------------------ exponentials, one thread per key
-    const int key = tid - 128;
-    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    // ------------------------------------------------------------------ exponentials, two threads per key, 64 heads each
+    const int key = (tid - 128) & 127, half = (tid - 128) >> 7, quad = warp & 3;
+    const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16) + 64 * half;
     uint32_t g = 0;
     int run = 0;
     bool ok = true;
     for (; ok && r.left > 0; r.next(p), ++run) {
-      float* ls = lse_sh + (run & 1) * kHeads;
-      ls[key] = __ldg(p.lse + r.tok * kHeads + key) * kLog2e;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      // the run's lse in units of log 2 (the four warps of a half write the same values; a warp two runs ahead of
+      // another cannot be: every tile needs all warps' release of the one before)
+      float* ls = lse_sh + (run & 1) * kHeads + 64 * half;
+      const float2 l2 = __ldg(reinterpret_cast<const float2*>(p.lse + r.tok * kHeads + 64 * half) + lane);
+      __syncwarp();
+      *reinterpret_cast<float2*>(ls + 2 * lane) = make_float2(l2.x * kLog2e, l2.y * kLog2e);
+      __syncwarp();
       for (int t = r.t0; ok && t < r.t1; ++t, ++g) {
         const int u = t * kTile + key;
         bool take = u < r.keys;
@@ -317,41 +331,55 @@ __global__ void __launch_bounds__(SELECTED ? 384 : 256, 1)
           row = __ldg(p.idx + r.tok * p.k + u);
           take = row >= 0 && row < p.S_max;
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[g % kAccs], (g / kAccs) & 1, &abort_flag, p.status,
-                                               DSA_SITE_WEIGHTS_ACC))) {
+        float z[64];
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {
+          if (part % kJoint == 0) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&acc_full[part / kJoint], g & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC));
+            if (!ok) break;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[32];
+            tmem_ld32(t_row + part * kHeads + 32 * c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              z[32 * c + i] = part == 0 ? __uint_as_float(x[i]) : z[32 * c + i] + __uint_as_float(x[i]);
+          }
+          if (part % kJoint == kJoint - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_empty[part / kJoint]);
+          }
+        }
+        if (!ok) break;
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(ls + i);
+          s4[0] += exp2_approx(fmaf(z[i], p.scale_log2, -l4.x));
+          s4[1] += exp2_approx(fmaf(z[i + 1], p.scale_log2, -l4.y));
+          s4[2] += exp2_approx(fmaf(z[i + 2], p.scale_log2, -l4.z));
+          s4[3] += exp2_approx(fmaf(z[i + 3], p.scale_log2, -l4.w));
+        }
+        float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        float* other = sum_sh + (g & 1) * kTile + key;
+        if (half == 1) {
+          *other = sum;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sum_full[quad]);
+          continue;
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&sum_full[quad], g & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC))) {
           ok = false;
           break;
         }
-        tc_fence_after();
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t x[2][32];
-        const uint32_t d = t_row + (g % kAccs) * kHeads;
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          tmem_ld32(d + 32 * c, x[0]);
-          tmem_ld32(d + 32 * c + 32, x[1]);
-          tmem_ld_wait();
-          if (c == 2) {                  // the scores are in registers: the accumulator may be overwritten
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[g % kAccs]);
-          }
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(ls + 32 * c + i);
-            const uint32_t* y = &x[i >> 5][i & 31];
-            s4[0] += exp2_approx(fmaf(__uint_as_float(y[0]), p.scale_log2, -l4.x));
-            s4[1] += exp2_approx(fmaf(__uint_as_float(y[1]), p.scale_log2, -l4.y));
-            s4[2] += exp2_approx(fmaf(__uint_as_float(y[2]), p.scale_log2, -l4.z));
-            s4[3] += exp2_approx(fmaf(__uint_as_float(y[3]), p.scale_log2, -l4.w));
-          }
-        }
-        if (u < r.keys) {
-          const float sum = take ? (s4[0] + s4[1]) + (s4[2] + s4[3]) : 0.f;
-          p.w[r.tok * p.ld + u] = sum;
-          // one query per sequence: no other weight meets this row's
-          if (take && p.T == 1 && p.acc_out) p.acc_out[r.tok * p.S_max + row] = p.acc[r.tok * p.S_max + row] + sum;
-        }
+        sum = take ? sum + *other : 0.f;
+        if (u < r.keys) p.w[r.tok * p.ld + u] = sum;
+        // one query per sequence: no other weight meets this row's
+        if (take && p.T == 1 && p.acc_out) p.acc_out[r.tok * p.S_max + row] = p.acc[r.tok * p.S_max + row] + sum;
       }
     }
   }
@@ -469,7 +497,7 @@ int launch_weights(const uint16_t* q, const WeightsParams& p, int64_t B, cudaStr
   }
   const int64_t tiles = p.BT * (((SELECTED ? p.k : p.S_max) + kTile - 1) / kTile);
   const unsigned grid = (unsigned)std::min<int64_t>(dsa_host::device_sm_count(), tiles);
-  const int rc = dsa_host::launch(mla_weights_kernel<SELECTED>, dim3(grid), dim3(SELECTED ? 384 : 256), kSmem, stream, q_map,
+  const int rc = dsa_host::launch(mla_weights_kernel<SELECTED>, dim3(grid), dim3(SELECTED ? 512 : 384), kSmem, stream, q_map,
                                   k_map, p);
   if (rc != DSA_OK) return rc;
   if (p.T == 1) return DSA_OK;
