@@ -423,7 +423,4 @@ bool encode_tensor_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, void* bas
 // dims[0] innermost; strides[i] = bytes between consecutive indices of dims[i + 1].
 bool encode_tensor_map_3d(CUtensorMap* map, CUtensorMapDataType dtype, void* base, const uint64_t dims[3],
                           const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swizzle);
-// the same for `rank` dimensions (2 to 5)
-bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, int rank, void* base, const uint64_t* dims,
-                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 }  // namespace dsa_host

@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "dsa.h"
 #include "kernels.h"
+#include "pair.cuh"
 
 namespace {
 

@@ -148,6 +148,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
 }  // namespace dsa
 
 namespace dsa_host {
+// encode_tensor_map_3d for `rank` dimensions (2 to 5); defined in dsa_abi.cu
+bool encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, int rank, void* base, const uint64_t* dims,
+                       const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
+
 // launch() for a grid of `clusters` clusters of `size` CTAs.
 template <typename... KArgs, typename... Args>
 int launch_clusters(void (*kernel)(KArgs...), unsigned size, unsigned clusters, unsigned threads, size_t smem,
