@@ -407,10 +407,8 @@ DSA_API int dsa_rope(const void* x, int dtype, int64_t rows, int heads, int64_t 
  *   workspace / ws_bytes: at least dsa_mla_shared_workspace_size(B, T, P, S_max) bytes; holds
  *           nothing between calls, and must not be shared by calls that overlap on the GPU
  * z = softmax_scale * q . key over the 576 features of the visible rows, out = softmax(z) . key[0:512].
- * A query that sees no row gets zeros and lse = -inf. Own rows that no query of their sequence
- * sees may hold anything, NaN included. (Among the queries of one sequence, a NaN or infinity in
- * a row that only the later of two adjacent queries sees may show in the earlier one's output too;
- * another sequence never sees it.)
+ * A query that sees no row gets zeros and lse = -inf. Own rows that a query does not see may hold
+ * anything, NaN included.
  * P + S_max >= 1; B * T <= 2^23; P and S_max at most DSA_MAX_POS; pointers 16-byte aligned.
  */
 DSA_API int dsa_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const uint16_t* kv,

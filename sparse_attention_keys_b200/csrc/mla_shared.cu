@@ -142,6 +142,24 @@ __device__ __forceinline__ Tile get_tile(const SharedParams& p, const Unit& x, i
   return r;
 }
 
+// What the value pair does with keys [kb, kb + 64) of a tile: one pass for both tokens where they see the
+// same number of them, else one for each that sees any. A pass multiplies only rows that its tokens see:
+// a hidden row may hold anything, and 0 * NaN is NaN.
+struct Pass {
+  int n;                 // rows
+  uint32_t off0, off1;   // lanes of token A / B: ~0 where their O stays as it is
+};
+__device__ __forceinline__ bool get_pass(const Tile& t, int kb, int j, Pass& r) {
+  const int a = max(0, min(64, t.nA - kb)), b = max(0, min(64, t.nB - kb));
+  const bool both = a == b, single = a == 0 || b == 0;
+  if (max(a, b) == 0 || j > (both || single ? 0 : 1)) return false;
+  const bool first = both || (single ? a > 0 : j == 0), second = both || (single ? b > 0 : j == 1);
+  r.n = first ? a : b;
+  r.off0 = first ? 0u : 0xffffffffu;
+  r.off1 = second ? 0u : 0xffffffffu;
+  return true;
+}
+
 // The pieces of a cluster's range of tiles, one unit after the other; every role walks it for itself.
 struct Walk {
   int64_t left;        // tiles left in the range
@@ -468,19 +486,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    auto v_slot = [&](const Tile& t, int kb, int half) {
-      const int n = t.most();
+    auto v_slot = [&](const Tile& t, int kb, int n, int half) {
       const uint32_t dst = ring + slot * kBlock, bar = cluster_addr(&full[slot], 2);
       const int block = 4 * half + 2 * (int)side;
-      if (t.src < 0 || n - kb >= 64) {
+      if (t.src < 0 || n >= 64) {
         if (el) {
           arrive_expect_tx_cluster(bar, kBlock);
           load_slot(&p_map, &s_map, t.src, t.k0 + kb, block, dst, bar);
         }
         return;
       }
-      // the rows behind the last visible key may hold anything, and 0 * NaN is NaN: the warp copies
-      // the visible rows itself and puts zeros behind them
+      // the warp copies the visible rows itself and puts zeros behind them
       const uint16_t* src = p.kv + ((int64_t)t.src * p.S_max + t.k0 + kb) * kDqk + 64 * block;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -488,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int r = 32 * h + 2 * i + (lane >> 4), c = lane & 15;    // row, 16-byte chunk of its 256 bytes
-          v[i] = r < n - kb ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * kDqk) + c) : make_uint4(0, 0, 0, 0);
+          v[i] = r < n ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)r * kDqk) + c) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -516,11 +532,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t > w.t0) k_tile(tile);
           continue;
         }
-        for (int i = 0; ok && 64 * (i >> 1) < tile.most(); ++i, advance()) {
-          if (turn != mine) continue;
-          acquire();
-          if (ok) v_slot(tile, 64 * (i >> 1), i & 1);
-        }
+        Pass pass;
+        for (int kb = 0; kb < kTile; kb += 64)
+          for (int j = 0; ok && get_pass(tile, kb, j, pass); ++j)
+            for (int half = 0; ok && half < 2; ++half, advance()) {
+              if (turn != mine) continue;
+              acquire();
+              if (ok) v_slot(tile, kb, pass.n, half);
+            }
       }
     }
     // the last MMAs' arrivals have to reach this CTA before it leaves
@@ -557,44 +576,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool startedA = false, startedB = false;
         for (int t = w.t0; ok && t < w.t1; ++t) {
           const Tile tile = get_tile(p, w.x, t);
-          // the token that sees nothing of the tile keeps its O
-          const uint32_t off0 = tile.nA > 0 ? 0u : 0xffffffffu, off1 = tile.nB > 0 ? 0u : 0xffffffffu;
-          const bool acc = (tile.nA > 0 && startedA) || (tile.nB > 0 && startedB);
-          startedA |= tile.nA > 0;
-          startedB |= tile.nB > 0;
-          const int n = tile.most();
           if (!wait(&p_ready[buf], pb, DSA_SITE_SHARED_P)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const bool plain = acc && (off0 | off1) == 0 && n == kTile;
+          Pass pass;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {                    // 64 keys x 256 features each
-            const int kb = 64 * (i >> 1);
-            if (kb >= n) break;
-            if (!wait(&full[slot], ph, DSA_SITE_SHARED_FULL)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            if (tile.src >= 0 && n - kb < 64) cluster_fence();       // both CTAs' warps wrote this slot
-            const uint64_t a = p_desc + (uint64_t)((2 * buf + (i >> 1)) * (kBlock >> 4));
-            const uint64_t b = v_desc + (uint64_t)(slot * (kBlock >> 4));
-            if (elect_one()) {
-              if (plain) {
+          for (int kb = 0; kb < kTile; kb += 64) {
+            for (int j = 0; ok && get_pass(tile, kb, j, pass); ++j) {
+              const bool acc = (pass.off0 == 0 && startedA) || (pass.off1 == 0 && startedB);
+              const bool plain = acc && (pass.off0 | pass.off1) == 0 && pass.n == 64;
+              startedA |= pass.off0 == 0;
+              startedB |= pass.off1 == 0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) pair_mma_ss(256 * (i & 1), a + 2 * k, b + 128 * k, idesc, 1);
-              } else {
-                for (int k = 0; k < 4 && kb + 16 * k < n; ++k)
-                  pair_mma_ss_masked(256 * (i & 1), a + 2 * k, b + 128 * k, idesc, off0, off1, acc || kb + k > 0);
+              for (int half = 0; half < 2; ++half) {         // 256 features each
+                if (!wait(&full[slot], ph, DSA_SITE_SHARED_FULL)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                if (tile.src >= 0 && pass.n < 64) cluster_fence();     // both CTAs' warps wrote this slot
+                const uint64_t a = p_desc + (uint64_t)((2 * buf + (kb >> 6)) * (kBlock >> 4));
+                const uint64_t b = v_desc + (uint64_t)(slot * (kBlock >> 4));
+                if (elect_one()) {
+                  if (plain) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) pair_mma_ss(256 * half, a + 2 * k, b + 128 * k, idesc, 1);
+                  } else {
+                    for (int k = 0; k < 4 && 16 * k < pass.n; ++k)
+                      pair_mma_ss_masked(256 * half, a + 2 * k, b + 128 * k, idesc, pass.off0, pass.off1, acc || k > 0);
+                  }
+                  pair_commit(&empty[slot], 12);
+                }
+                __syncwarp();
+                if (++slot == kSlots) {
+                  slot = 0;
+                  ph ^= 1;
+                }
               }
-              pair_commit(&empty[slot], 12);
-            }
-            __syncwarp();
-            if (++slot == kSlots) {
-              slot = 0;
-              ph ^= 1;
             }
           }
           if (ok && elect_one()) pair_commit(&pv_done[buf], 15);

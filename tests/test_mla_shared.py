@@ -149,6 +149,30 @@ def test_hidden_rows_may_hold_anything(T, P):
 
 
 @gpu
+@pytest.mark.parametrize("P", [0, 200])
+def test_a_row_that_only_a_later_query_sees(P):
+    """A NaN or infinity there is the later query's alone, wherever in a tile the two part."""
+    for n in (2, 20, 64, 65, 100, 128, 129, 200):
+        q, prefix, kv, q_pos, kv_len = make(2, 2, P, 256, seed=n, lens=[n, n])
+        clean = dsa.dsa_mla_shared(q, prefix, kv, q_pos, kv_len)
+        for fill in (float("nan"), float("inf")):
+            kv[0, n - 1, 7] = fill
+            got = dsa.dsa_mla_shared(q, prefix, kv, q_pos, kv_len)
+            assert torch.equal(got[0][0, 0], clean[0][0, 0]) and torch.equal(got[1][0, 0], clean[1][0, 0])
+            assert torch.equal(got[0][1], clean[0][1]) and bool(got[0][0, 1].isnan().any())
+
+
+@gpu
+def test_queries_of_a_sequence_far_apart():
+    """Positions in any order: neighbours that part in different tiles, one that sees nothing."""
+    q, prefix, kv, _, kv_len = make(3, 4, 70, 400, seed=21, lens=[400, 399, 256])
+    q_pos = torch.tensor([[399, 3, -1, 200], [130, 131, 64, 63], [255, 127, 128, 0]], dtype=torch.int32, device="cuda")
+    for pre in (prefix, None):
+        out, lse = dsa.dsa_mla_shared(q, pre, kv, q_pos, kv_len)
+        check(out, lse, q, pre, kv, q_pos, kv_len)
+
+
+@gpu
 def test_large_scores_move_the_maximum():
     """Keys that grow along the row: the running maximum moves at every tile, by up to 2^100."""
     q, prefix, kv, q_pos, kv_len = make(3, 1, 600, 200, seed=7, lens=[200, 111, 1])
