@@ -544,6 +544,8 @@ def _arg(t, name, dtype, shape, device):
     """Address of a contiguous `dtype` tensor of `shape` on `device`, a CUDA device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -552,9 +554,7 @@ def _arg(t, name, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}: all tensors must be on one device")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, not on {device}: all tensors must be on one device")
 
 
 def _maybe(t, name, dtype, shape, device):
@@ -596,6 +596,13 @@ def dsa_rope_freqs(pairs: int, theta: float = 10000.0, factor: float = 1.0, orig
 _ROPE_DTYPES = {torch.float32: DSA_F32, torch.bfloat16: DSA_BF16, torch.float16: DSA_F16}
 
 
+def _rope_strides(t, name, rows, heads, dim):
+    st = t.stride()
+    if dim > 1 and st[-1] != 1:
+        raise ValueError(f"the features of {name} must be contiguous")
+    return st[0] if rows > 1 else heads * dim, st[1] if heads > 1 else dim
+
+
 def dsa_rope(x, pos, freqs, offset: int = 0, interleaved: bool = False, inverse: bool = False, scale: float = 1.0,
              out=None, stream=None):
     """x fp32, bf16 or fp16 [rows, heads, dim] or [rows, dim], features contiguous, rows and heads at any stride;
@@ -607,50 +614,50 @@ def dsa_rope(x, pos, freqs, offset: int = 0, interleaved: bool = False, inverse:
         raise TypeError("x must be a float32, bfloat16 or float16 tensor")
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    shape = x.shape
-    if len(shape) not in (2, 3):
+    device = x.device
+    if stream is not None or device.index != torch.cuda.current_device():
+        return _launch(device, stream, lambda s: _rope(x, pos, freqs, offset, interleaved, inverse, scale, out, s))
+    return _rope(x, pos, freqs, offset, interleaved, inverse, scale, out, torch._C._cuda_getCurrentRawStream(device.index))
+
+
+def _rope(x, pos, freqs, offset, interleaved, inverse, scale, out, s):
+    device, shape = x.device, x.shape
+    if len(shape) == 3:
+        rows, heads, dim = shape
+    elif len(shape) == 2:
+        (rows, dim), heads = shape, 1
+    else:
         raise ValueError(f"x must be [rows, heads, dim] or [rows, dim], got {list(shape)}")
-    rows, dim = shape[0], shape[-1]
-    heads = shape[1] if len(shape) == 3 else 1
     (pairs,) = _dims(freqs, "freqs", torch.int64, 1)
     if pairs < 1 or offset < 0 or offset + 2 * pairs > dim:
         raise ValueError(f"features [{offset}, {offset + 2 * pairs}) do not lie in a head of {dim}")
-    device = x.device
     pos_ptr = _arg(pos, "pos", torch.int32, (rows,), device)
     freqs_ptr = _arg(freqs, "freqs", torch.int64, (pairs,), device)
-    if out is not None:
+    xr, xh = _rope_strides(x, "x", rows, heads, dim)
+    xp = x.data_ptr()
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=device)
+        yp, yr, yh = out.data_ptr(), heads * dim, dim
+    else:
         if not isinstance(out, torch.Tensor) or out.dtype is not x.dtype:
             raise TypeError(f"out must be a {x.dtype} tensor")
         if out.shape != shape or out.device != device:
             raise ValueError(f"out must be {list(shape)} on {device}, got {list(out.shape)} on {out.device}")
-
-    def strides(t, name):
-        st = t.stride()
-        if dim > 1 and st[-1] != 1:
-            raise ValueError(f"the features of {name} must be contiguous")
-        return st[0] if rows > 1 else heads * dim, st[1] if len(shape) == 3 and heads > 1 else dim
-
-    def call(s):
-        y = torch.empty(shape, dtype=x.dtype, device=device) if out is None else out
-        if rows == 0 or heads == 0:
-            return y
-        (xr, xh), (yr, yh) = strides(x, "x"), strides(y, "out")
-        xp, yp = x.data_ptr(), y.data_ptr()
-        if out is not None and (xp != yp or xr != yr or xh != yh):
-            size = x.element_size()
-            x_end, y_end = (xp + size * ((rows - 1) * xr + (heads - 1) * xh + dim),
-                            yp + size * ((rows - 1) * yr + (heads - 1) * yh + dim))
-            if xp < y_end and yp < x_end:
-                # the memory they span meets: they may still be different columns of the same rows
-                gap = (yp - xp) // size % xr if xr == yr and xr > 0 else 0
-                if gap < (heads - 1) * xh + dim or gap + (heads - 1) * yh + dim > xr:
-                    raise ValueError("out must be x itself or not overlap it")
-        flags = (DSA_ROPE_INTERLEAVED if interleaved else 0) | (DSA_ROPE_INVERSE if inverse else 0)
-        _check(_lib.dsa_rope(xp, _ROPE_DTYPES[x.dtype], rows, heads, xr, xh, dim, offset, pairs, pos_ptr, freqs_ptr, scale,
-                             flags, yp, yr, yh, s), "dsa_rope")
-        return y
-
-    return _launch(device, stream, call)
+        yr, yh = _rope_strides(out, "out", rows, heads, dim)
+        yp = out.data_ptr()
+    if rows == 0 or heads == 0:
+        return out
+    if xp != yp or xr != yr or xh != yh:
+        size, wide_x, wide_y = x.element_size(), (heads - 1) * xh + dim, (heads - 1) * yh + dim
+        if xp < yp + size * ((rows - 1) * yr + wide_y) and yp < xp + size * ((rows - 1) * xr + wide_x):
+            # the memory they span meets: they may still be different columns of the same rows
+            gap = (yp - xp) // size % xr if xr == yr and xr > 0 else 0
+            if gap < wide_x or gap + wide_y > xr:
+                raise ValueError("out must be x itself or not overlap it")
+    flags = (DSA_ROPE_INTERLEAVED if interleaved else 0) | (DSA_ROPE_INVERSE if inverse else 0)
+    _check(_lib.dsa_rope(xp, _ROPE_DTYPES[x.dtype], rows, heads, xr, xh, dim, offset, pairs, pos_ptr, freqs_ptr, scale, flags,
+                         yp, yr, yh, s), "dsa_rope")
+    return out
 
 
 def dsa_mla_shared_workspace_size(B: int, T: int, P: int, S_max: int) -> int:

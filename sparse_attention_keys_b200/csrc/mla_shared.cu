@@ -520,8 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (; ok && w.valid(); w.next(p)) {
       if (w.empty(p)) continue;
       if (!values) {
-        if (piece == 0 && mine == 0 && el) q_tma(0);
-        __syncwarp();
         k_tile(get_tile(p, w.x, w.t0));
         ok = ok && q_rows(piece);
       }
@@ -642,6 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int tok = 2 * w.u + (int)side;
       const bool some = !w.empty(p);
       if (some && piece == 0) {                            // three blocks of 64 features of the first Q
+        if (warp == 4 && elect_one()) q_tma(0);
+        __syncwarp();
         if (!__all_sync(0xffffffffu, mbar_wait(q_stage, 0, &abort_flag, p.status, DSA_SITE_SHARED_Q))) break;
 #pragma unroll 1
         for (int f = 3 * group; f < 3 * group + 3; ++f) {
