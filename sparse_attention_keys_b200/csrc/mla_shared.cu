@@ -21,6 +21,10 @@
 // most two such pieces, so the workspace is bounded whatever the lengths are, and the device alone
 // reads the lengths.
 //
+// Measured: 2620 cycles a tile, 88% of it the score pair's MMAs. 512 queries over 16384 shared rows take 1.89 ms,
+// 1.24 PFLOP/s (75% of the measured matrix rate; the clock falls under the power limit), 64 queries over 8192
+// shared and up to 512 own rows 143 us. Four-CTA clusters leave 16 SMs idle.
+//
 // Score CTA: Q features 0..511 in TMEM [0, 256) (A operand, bf16 pairs), 512..575 in shared memory;
 // two score buffers in TMEM [256, 512); three staging buffers for P; K through a ring of 16 KB slots
 // (64 keys x 128 features, this CTA's half of the tile's keys, five slots a tile).
@@ -216,8 +220,8 @@ static_assert(kBars * 8 <= 512, "room for the barriers");
 // The Q K^T of a piece, issued by one warp of rank 0 (`done` tiles came before). The loops and waits are the
 // whole warp's and every value in them the same in all lanes, only the MMAs are one thread's: then their
 // operands stay in uniform registers and an MMA takes its 65 cycles to issue. (With the loops inside the one
-// thread's branch it took about 120: 4.0 instead of 2.65 million cycles for shared_chunk.) For the same reason
-// TMEM addresses are constants: a CTA that allocates all 512 columns gets them from column 0 on.
+// thread's branch it took about 120: 4000 instead of 2620 cycles a tile.) For the same reason TMEM addresses
+// are constants: a CTA that allocates all 512 columns gets them from column 0 on.
 __device__ __forceinline__ bool issue_scores(uint8_t* smem, uint64_t* bars, uint32_t done, uint32_t tiles, uint32_t parity,
                                              int* abort_flag, int* status) {
   const uint32_t idesc = idesc_f32acc(1, 1, 256, kTile, 0, 0);
@@ -393,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   long long lo = min(total, share * cluster), count = min(total - lo, share);
   // A cut inside a share costs its cluster another Q, another pipeline fill and 256 KB of fp32 per value CTA, about 8
   // tiles: where there are no more units than clusters, every unit gets the same number of clusters and an equal
-  // share in each, if the longest share is not that much longer (shared_b64: 72 against 67 tiles, no cuts at
-  // all; shared_b8: eight clusters a unit).
+  // share in each, if the longest share is not that much longer (64 queries over 8192 shared rows: 72 against 67
+  // tiles and no cuts at all, 167 -> 145 us; 8 queries over 1031: eight clusters a unit).
   const int group = units <= clusters ? (int)((uint32_t)clusters / (uint32_t)units) : 1;
   const int part = (int)((uint32_t)(longest + group - 1) / (uint32_t)group);
   if (units <= clusters && part <= share + 8) {
@@ -627,8 +631,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (!values) {
     // ------------------------------------------------------------------ softmax: one thread per row, two warpgroups that
-    // take the tiles in turn. A tile takes a warpgroup about 3500 cycles, so one alone would be slower
-    // than its MMAs (2306). The running maximum passes from one to the other as soon as it is known.
+    // take the tiles in turn. A tile takes a warpgroup about 3500 cycles, 4300 beside the other (1024 of MUFU each),
+    // so one alone would be slower than the MMAs (2306). The running maximum passes from one to the other as soon
+    // as it is known.
     const int row = (tid - 128) & 127, group = (tid - 128) >> 7, quad = warp & 3;    // row: head, TMEM lane
     const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t peer = rank + 2;
@@ -922,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the pieces of units that were cut. A unit's first piece is the last one of some cluster c, the others
 // are the first ones of the clusters behind it. The blocks take (cut unit, 32 rows x 64 features) in turn: most
-// clusters head no unit, and a block for each of them cost more than the joining (20 us for shared_b8).
+// clusters head no unit, and blocks for all of them took longer than the joining (10 of 40 us for 8 queries).
 __global__ void __launch_bounds__(256) mla_shared_join_kernel(const SharedParams p, int clusters) {
   extern __shared__ float2 ml_sh[];      // [pieces][32 rows]: maximum, sum
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1094,8 +1099,8 @@ int launch_mla_shared(const uint16_t* q, const uint16_t* prefix, int P, const ui
   }
   int rc = dsa_host::launch_clusters(mla_shared_kernel, 4, (unsigned)clusters, kThreads, kSmem, stream, q_map, pm, sm, p);
   if (rc != DSA_OK) return rc;
-  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)(2 * dsa_host::device_sm_count())), dim3(256), (size_t)clusters * 32 * 8, stream,
-                          p, clusters);
+  return dsa_host::launch(mla_shared_join_kernel, dim3((unsigned)(2 * dsa_host::device_sm_count())), dim3(256),
+                          (size_t)clusters * 32 * 8, stream, p, clusters);
 }
 
 }  // namespace dsa
