@@ -5,11 +5,13 @@
 // attention returned, for the visible rows (dense) or for the selected ones (w[b][t][u] for slot u).
 //
 // The scores are computed transposed, S^T = K Q^T, so that a TMEM lane holds one key and the 128
-// columns its heads: the sum over the heads stays inside a thread. One CTA per SM takes an equal
-// share of all (query, 128-key tile) pairs; the query (128 x 576, 144 KB) stays in shared memory while
-// 16 KB blocks of keys (128 keys x 64 features) pass through a ring of five. Per tile: 36 MMAs of
-// 128 x 128 x 16 (65 cycles each, 2340) and 128 x 128 exponentials (1024 cycles of MUFU). For one query
-// per sequence HBM is the bound: 147 KB a tile take an SM's share of it 6300 cycles.
+// columns its heads: the sum over the heads stays inside a thread pair. A CTA pair (cta_group::2, M = 256
+// keys, 128 per CTA) takes an equal share of all (query, 256-key tile) pairs; each CTA keeps 64 heads of
+// the query in shared memory (72 KB) while 32 KB slots of its keys (128 keys x 128 features) pass through a
+// ring of four. Per tile: 36 MMAs of 256 x 128 x 16 (65 cycles each, 2340) and 128 x 128 exponentials per
+// CTA (1024 cycles of MUFU). For one query per sequence HBM is the bound: a CTA's 147 KB a tile take an SM's
+// share of it 6300 cycles, and the ring's 128 KB cover its latency (45 us for 64 queries over 2048 to 4096
+// rows each, 5.0 TB/s; a CTA alone, with all heads and an 80 KB ring, 47 us).
 //
 // A tile's contraction is cut into four parts of 128, 128, 128 and 192 features, each with an accumulator
 // of 128 columns of its own, that are added in registers. The exponential turns an absolute error of the score
@@ -18,8 +20,9 @@
 // (fp32 matrix products leave 2e-6). It costs 5% of the time.
 //
 // Selected rows are gathered by four warps with 16-byte cp.async into the swizzled operand layout,
-// 128 bytes of each row per block. (Hinting whole rows into L2 a tile ahead was slower, 46.5 against
-// 43.5 us for 64 queries of 2048 rows; so was hinting the next dense tile, 55 against 50 us.)
+// 256 bytes of each row per slot; a fifth hands the slots that have landed to the leader. (Hinting whole rows
+// into L2 a tile ahead was slower, 46.5 against 43.5 us for 64 queries of 2048 rows; so was hinting the next
+// dense tile, 55 against 50 us.)
 #include <math.h>
 
 #include <algorithm>
@@ -31,16 +34,20 @@ namespace dsa {
 
 namespace {
 
-constexpr int kHeads = 128, kDqk = 576, kTile = 128;
-constexpr int kBlock = 128 * 128;                  // 16 KB: 64 features of 128 rows
-constexpr int kSlots = 5;
-constexpr int kOffRing = 9 * kBlock;
-constexpr int kOffBar = kOffRing + kSlots * kBlock;
+constexpr int kHeads = 128, kDqk = 576;
+constexpr int kRows = 128;                         // keys of a tile on each CTA of a pair
+constexpr int kTile = 2 * kRows;
+constexpr int kQBlock = 64 * 128;                  // 8 KB: 64 features of this CTA's 64 heads
+constexpr int kBlock = kRows * 128;                // 16 KB: 64 features of 128 keys
+constexpr int kSlot = 2 * kBlock;
+constexpr int kSlots = 4;
+constexpr int kOffRing = 9 * kQBlock;
+constexpr int kOffBar = kOffRing + kSlots * kSlot;
 constexpr int kOffLse = kOffBar + 256;             // [2][128] fp32
 constexpr int kOffSum = kOffLse + 2 * 128 * 4;     // [2][128] fp32
 constexpr int kOffScan = kOffSum + 2 * 128 * 4;    // set-up words
-constexpr int kSmem = kOffScan + 256;
-static_assert(kSmem <= 232448, "shared memory per CTA");
+constexpr int kSmem = 1024 + kOffScan + 256;
+static_assert(kOffRing % 1024 == 0 && kSmem <= 232448, "shared memory per CTA");
 constexpr int kParts = 4;                          // parts of a contraction, an accumulator of 128 columns each
 constexpr int kGatherWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -48,6 +55,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 }  // namespace
 
 struct WeightsParams {
+  const uint16_t* q;
   const uint16_t* kv;
   const int32_t* idx;      // [B][T][k] (selected rows), or NULL (dense)
   const float* lse;        // [B][T][128]
@@ -117,13 +125,14 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
   // 111 one by one), one where the gather is (64 queries of 2048 rows: 43.5 us, and 46 by twos).
   constexpr int kJoint = SELECTED ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = smem_raw;              // 1024-byte aligned: the kernel has no other shared memory
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint64_t* full = bars;                 // [kSlots] keys landed
+  uint64_t* full = bars;                 // leader [kSlots]: both CTAs' keys landed
   uint64_t* empty = full + kSlots;       // [kSlots] their MMAs are done
-  uint64_t* acc_full = empty + kSlots;   // [kParts / kJoint] parts of the scores ready
-  uint64_t* acc_empty = acc_full + kParts;  // [kParts / kJoint] they are read
-  uint64_t* q_full = acc_empty + kParts;
+  uint64_t* gathered = empty + kSlots;   // [kSlots] this CTA's keys landed (selected rows)
+  uint64_t* acc_full = gathered + kSlots;  // [kParts / kJoint] parts of the scores ready
+  uint64_t* acc_empty = acc_full + kParts;  // leader [kParts / kJoint]: both CTAs have read them
+  uint64_t* q_full = acc_empty + kParts;   // leader: both halves of the query landed
   uint64_t* q_empty = q_full + 1;        // the run's MMAs are done
   uint64_t* sum_full = q_empty + 1;      // [4] the second half of the heads is summed, per quadrant
   float* lse_sh = reinterpret_cast<float*>(smem + kOffLse);
@@ -134,100 +143,141 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
   int& abort_flag = *reinterpret_cast<int*>(start_sh + 3);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
     abort_flag = 0;
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&full[s], SELECTED ? kGatherWarps * 32 : 1);
+      mbar_init(&full[s], 2);
       mbar_init(&empty[s], 1);
+      mbar_init(&gathered[s], kGatherWarps * 32);
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&acc_full[i], 1);
-      mbar_init(&acc_empty[i], 8);
+      mbar_init(&acc_empty[i], 16);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&sum_full[i], 1);
-    mbar_init(q_full, 1);
+    mbar_init(q_full, 2);
     mbar_init(q_empty, 1);
     fence_barrier_init();
     start_sh[0] = start_sh[1] = 0;
   }
-  if (warp == 2) {
-    tmem_alloc(&tmem_base_sh, 512);
-    tmem_relinquish();
-  }
+  if (warp == 2) pair_tmem_alloc(&tmem_base_sh, 512);
+  __syncwarp();
+  cluster_arrive();                      // this thread's part of the set-up; waited for below
   grid_dep_wait();
   grid_dep_launch();
 
-  // this CTA's share: thread i sums the tiles of the queries [i * per, (i + 1) * per)
-  const int64_t per = (p.BT + kThreads - 1) / kThreads;
-  const int64_t ua = min(p.BT, tid * per), ub = min(p.BT, ua + per);
-  long long sum = 0;
-  for (int64_t u = ua; u < ub; ++u) sum += tiles_of(p, u);
-  long long pre = sum;
+  // This pair's share of the tiles. Selections all have the same number; otherwise thread i sums the tiles of the
+  // queries [i * per, (i + 1) * per).
+  long long count, first_tok, first_tile;
+  if (SELECTED) {
+    const uint32_t each = (uint32_t)(p.k + kTile - 1) / kTile;
+    const long long total = p.BT * each, lo = total * pair / pairs;
+    count = total * (pair + 1) / pairs - lo;
+    first_tok = lo / each;
+    first_tile = lo - first_tok * each;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  } else {
+    const int64_t per = (p.BT + kThreads - 1) / kThreads;
+    const int64_t ua = min(p.BT, tid * per), ub = min(p.BT, ua + per);
+    long long sum = 0;
+    for (int64_t u = ua; u < ub; ++u) sum += tiles_of(p, u);
+    long long pre = sum;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, pre, d);
-    if (lane >= d) pre += o;
-  }
-  if (lane == 31) scan_sh[warp] = pre;
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  long long total = 0, base = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w == warp) base = total;
-    total += scan_sh[w];
-  }
-  const long long excl = base + pre - sum;
-  const long long lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-  if (sum > 0 && lo >= excl && lo < excl + sum) {
-    long long off = lo - excl;
-    int64_t u = ua;
-    for (; u < ub; ++u) {
-      const int n = tiles_of(p, u);
-      if (off < n) break;
-      off -= n;
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long o = __shfl_up_sync(0xffffffffu, pre, d);
+      if (lane >= d) pre += o;
     }
-    start_sh[0] = u;
-    start_sh[1] = off;
+    if (lane == 31) scan_sh[warp] = pre;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    long long total = 0, base = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w == warp) base = total;
+      total += scan_sh[w];
+    }
+    const long long excl = base + pre - sum;
+    const long long lo = total * pair / pairs;
+    count = total * (pair + 1) / pairs - lo;
+    if (sum > 0 && lo >= excl && lo < excl + sum) {
+      long long off = lo - excl;
+      int64_t u = ua;
+      for (; u < ub; ++u) {
+        const int n = tiles_of(p, u);
+        if (off < n) break;
+        off -= n;
+      }
+      start_sh[0] = u;
+      start_sh[1] = off;
+    }
+    __syncthreads();
+    first_tok = start_sh[0];
+    first_tile = start_sh[1];
   }
-  __syncthreads();
+  cluster_wait();                        // both CTAs' barriers are initialised, both hold their TMEM
   const uint32_t tmem = tmem_base_sh;
   const uint32_t ring = smem_u32(smem + kOffRing);
   Runs r;
-  r.start(p, start_sh[0], start_sh[1], hi - lo);
+  r.start(p, first_tok, first_tile, count);
 
   if (warp == 0) {
-    // ------------------------------------------------------------------ TMA: queries, and dense keys
+    // ------------------------------------------------------------------ TMA: queries (64 heads a CTA), and dense keys
     if (elect_one()) {
       int slot = 0, run = 0;
       uint32_t ph = 1;                   // a fresh slot counts as freed
       bool ok = true;
+      auto acquire = [&]() {
+        if (!mbar_wait(&empty[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY)) ok = false;
+        return ok;
+      };
+      auto advance = [&]() {
+        if (++slot == kSlots) {
+          slot = 0;
+          ph ^= 1;
+        }
+      };
       for (; ok && r.left > 0; r.next(p), ++run) {
-        if (run > 0 && !mbar_wait(q_empty, (run + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY)) break;
-        mbar_arrive_expect_tx(q_full, 9 * kBlock);
-        for (int f = 0; f < 9; ++f) tma_load_2d(smem + f * kBlock, &q_map, q_full, 64 * f, (int32_t)(r.tok * kHeads));
+        if (run > 0 && !mbar_wait(q_empty, (run + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY)) {
+          ok = false;
+          break;
+        }
+        const uint32_t q_bar = cluster_addr(q_full, 0);
+        arrive_expect_tx_cluster(q_bar, 9 * kQBlock);
+        for (int f = 0; f < 9; ++f)
+          pair_load_2d(smem_u32(smem) + f * kQBlock, &q_map, q_bar, 64 * f, (int32_t)(r.tok * kHeads + 64 * rank));
+        if (r.left > r.t1 - r.t0 && r.tok + 1 < p.BT)            // the next run's, into L2
+          for (int i = 0; i < 9; ++i)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             p.q + ((r.tok + 1) * kHeads + 64 * rank) * kDqk + i * (kQBlock / 2)),
+                         "r"(kQBlock)
+                         : "memory");
         if (SELECTED) continue;
         const int b = (int)(r.tok / p.T);
         for (int t = r.t0; ok && t < r.t1; ++t)
-          for (int f = 0; f < 9; ++f) {
-            if (!mbar_wait(&empty[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY)) {
-              ok = false;
-              break;
-            }
-            mbar_arrive_expect_tx(&full[slot], kBlock);
-            tma_load_3d(smem + kOffRing + slot * kBlock, &k_map, &full[slot], 64 * f, t * kTile, b);
-            if (++slot == kSlots) {
-              slot = 0;
-              ph ^= 1;
+          for (int f = 0; f < 9 && acquire(); f += 2, advance()) {
+            const uint32_t bar = cluster_addr(&full[slot], 0);
+            const int row = t * kTile + rank * kRows;
+            if (row < r.keys) {
+              arrive_expect_tx_cluster(bar, kSlot);            // there is no block 9: zeros
+              pair_load_4d(ring + slot * kSlot, &k_map, bar, 0, row, f, b);
+            } else {
+              arrive_cluster(bar);       // no key of the tile on this CTA: its scores are not used
             }
           }
       }
+      // the last MMAs' arrivals have to reach this CTA before it leaves
+      if (!SELECTED)
+        for (int i = 0; i < kSlots && acquire(); ++i) advance();
+      if (ok && run > 0) mbar_wait(q_empty, (run + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issue, one thread
-    if (elect_one()) {
-      const uint32_t idesc = idesc_f32acc(1, 1, 128, kHeads, 0, 0);
+    // ------------------------------------------------------------------ MMA issue, one thread of the leader
+    if (rank == 0 && elect_one()) {
+      const uint32_t idesc = idesc_f32acc(1, 1, 256, kHeads, 0, 0);
       const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(ring);
       int slot = 0, run = 0;
       uint32_t ph = 0, g = 0;
@@ -238,44 +288,72 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
         const int tiles = r.t1 - r.t0;
         for (int t = 0; ok && t < tiles; ++t, ++g) {
 #pragma unroll
-          for (int f = 0; f < 9; ++f) {
-            const int part = f < 8 ? f >> 1 : kParts - 1;
-            const bool first = (f & 1) == 0 && f < 8;        // of its part
-            if (!ok || (first && part % kJoint == 0 && !mbar_wait(&acc_empty[part / kJoint], (g + 1) & 1, &abort_flag, p.status,
+          for (int f = 0; f < 9; f += 2) {                     // a slot is a part; the last one adds to the fourth
+            const int part = f < 8 ? f / 2 : kParts - 1;
+            if (!ok || (f < 8 && part % kJoint == 0 && !mbar_wait(&acc_empty[part / kJoint], (g + 1) & 1, &abort_flag, p.status,
                                                                   DSA_SITE_WEIGHTS_ACC)) ||
                 !mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL)) {
               ok = false;
               break;
             }
-            if (SELECTED) fence_proxy_async_smem();
+            if (SELECTED) cluster_fence();                     // both CTAs' threads wrote this slot
             tc_fence_after();
-            const uint64_t a = k_desc + (uint64_t)(slot * (kBlock >> 4)), b = q_desc + (uint64_t)(f * (kBlock >> 4));
+            const uint64_t a = k_desc + (uint64_t)(slot * (kSlot >> 4)), b = q_desc + (uint64_t)(f * (kQBlock >> 4));
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_f16_ss(part * kHeads, a + 2 * k, b + 2 * k, idesc, k > 0 || !first);
-            mma_commit(&empty[slot]);
-            if (f == 8 || ((f & 1) != 0 && f < 7 && part % kJoint == kJoint - 1)) mma_commit(&acc_full[part / kJoint]);
+            for (int k = 0; k < (f < 8 ? 8 : 4); ++k)
+              pair_mma_ss(part * kHeads, a + 2 * (k & 3) + (k >> 2) * (kBlock >> 4), b + 2 * (k & 3) + (k >> 2) * (kQBlock >> 4),
+                          idesc, k > 0 || f == 8);
+            pair_commit(&empty[slot], 3);
+            if (f == 8 || (f < 6 && part % kJoint == kJoint - 1)) pair_commit(&acc_full[part / kJoint], 3);
             if (++slot == kSlots) {
               slot = 0;
               ph ^= 1;
             }
           }
         }
-        if (ok) mma_commit(q_empty);
+        if (ok) pair_commit(q_empty, 3);
       }
-      if (ok && run > 0) mbar_wait(q_empty, (run + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY);
     }
+  } else if (SELECTED && warp == 2) {
+    // ------------------------------------------------------------------ hands gathered slots to the leader
+    int slot = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (; ok && r.left > 0; r.next(p))
+      for (int i = 0; ok && i < 5 * (r.t1 - r.t0); ++i) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&gathered[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL));
+        if (!ok) break;
+        fence_proxy_async_smem();        // cp.async writes -> MMA reads
+        cluster_fence();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(cluster_addr(&full[slot], 0));
+        if (++slot == kSlots) {
+          slot = 0;
+          ph ^= 1;
+        }
+      }
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ gather (selected rows)
-    // warp v copies rows 32 v .. 32 v + 31 of the tile: lane i holds the row number of row 32 v + i
+    // warp v copies rows 32 v .. 32 v + 31 of this CTA's half of the tile: lane i holds the row number of row 32 v + i
     const int v = warp - 12;
     int slot = 0;
     uint32_t ph = 1;
     bool ok = true;
+    auto acquire = [&]() {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&empty[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY));
+      return ok;
+    };
+    auto advance = [&]() {
+      if (++slot == kSlots) {
+        slot = 0;
+        ph ^= 1;
+      }
+    };
     for (; ok && r.left > 0; r.next(p)) {
       const uint16_t* kv = p.kv + r.tok / p.T * p.S_max * kDqk;
       const int32_t* idx = p.idx + r.tok * p.k;
       auto row_of = [&](int t) {
-        const int u = t * kTile + 32 * v + lane;
+        const int u = t * kTile + rank * kRows + 32 * v + lane;
         const int row = t < r.t1 && u < p.k ? __ldg(idx + u) : -1;
         if (row >= p.S_max) set_status(p.status, DSA_ERR_DEVICE_BOUNDS);
         return row < p.S_max ? row : -1;
@@ -283,31 +361,27 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
       int row = row_of(r.t0);
       for (int t = r.t0; ok && t < r.t1; ++t) {
         const int next = row_of(t + 1);
-        for (int f = 0; f < 9; ++f) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_EMPTY))) {
-            ok = false;
-            break;
-          }
-          const uint32_t dst = ring + slot * kBlock;
+        for (int f = 0; f < 9 && acquire(); f += 2, advance()) {
+          const uint32_t dst = ring + slot * kSlot;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            // four rows per step, eight 16-byte chunks each; rows that take no part are zeros
+            // four rows per step, eight 16-byte chunks of each of two blocks; rows that take no part are zeros
             const int rr = 4 * i + (lane >> 3), c = lane & 7;
             const int src = __shfl_sync(0xffffffffu, row, rr);
             const int at = 32 * v + rr;
-            cp_async_16_zfill(dst + at * 128 + ((c ^ (at & 7)) << 4), kv + (int64_t)max(src, 0) * kDqk + 64 * f + 8 * c,
-                              src >= 0);
+            const uint32_t to = dst + at * 128 + ((c ^ (at & 7)) << 4);
+            const uint16_t* from = kv + (int64_t)max(src, 0) * kDqk + 64 * f + 8 * c;
+            cp_async_16_zfill(to, from, src >= 0);
+            if (f < 8) cp_async_16_zfill(to + kBlock, from + 64, src >= 0);
           }
-          cp_async_mbar_arrive(&full[slot]);
-          if (++slot == kSlots) {
-            slot = 0;
-            ph ^= 1;
-          }
+          cp_async_mbar_arrive(&gathered[slot]);
         }
         row = next;
       }
     }
     cp_async_wait_all();
+    // the last MMAs' arrivals have to reach this CTA before it leaves
+    for (int i = 0; i < kSlots && acquire(); ++i) advance();
   } else if (warp >= 4) {
     // ------------------------------------------------------------------ exponentials, two threads per key, 64 heads each
     const int key = (tid - 128) & 127, half = (tid - 128) >> 7, quad = warp & 3;
@@ -324,13 +398,17 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
       *reinterpret_cast<float2*>(ls + 2 * lane) = make_float2(l2.x * kLog2e, l2.y * kLog2e);
       __syncwarp();
       for (int t = r.t0; ok && t < r.t1; ++t, ++g) {
-        const int u = t * kTile + key;
+        const int u = t * kTile + rank * kRows + key;
         bool take = u < r.keys;
         int row = u;
         if (SELECTED && take) {
           row = __ldg(p.idx + r.tok * p.k + u);
           take = row >= 0 && row < p.S_max;
         }
+        // dense, one query per sequence: the row's total is read ahead of the scores (the gathering kernel has no registers
+        // left for it)
+        const bool add = half == 0 && take && p.T == 1 && p.acc_out != nullptr;
+        const float before = !SELECTED && add ? p.acc[r.tok * p.S_max + row] : 0.f;
         float z[64];
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
@@ -351,7 +429,7 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
           if (part % kJoint == kJoint - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[part / kJoint]);
+            if (lane == 0) arrive_cluster(cluster_addr(&acc_empty[part / kJoint], 0));
           }
         }
         if (!ok) break;
@@ -365,7 +443,7 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
           s4[3] += exp2_approx(fmaf(z[i + 3], p.scale_log2, -l4.w));
         }
         float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-        float* other = sum_sh + (g & 1) * kTile + key;
+        float* other = sum_sh + (g & 1) * kRows + key;
         if (half == 1) {
           *other = sum;
           __syncwarp();
@@ -379,7 +457,7 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
         sum = take ? sum + *other : 0.f;
         if (u < r.keys) p.w[r.tok * p.ld + u] = sum;
         // one query per sequence: no other weight meets this row's
-        if (take && p.T == 1 && p.acc_out) p.acc_out[r.tok * p.S_max + row] = p.acc[r.tok * p.S_max + row] + sum;
+        if (add) p.acc_out[r.tok * p.S_max + row] = (SELECTED ? p.acc[r.tok * p.S_max + row] : before) + sum;
       }
     }
   }
@@ -398,7 +476,9 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 2) tmem_dealloc(tmem, 512);
+  cluster_arrive();                      // nothing of the pair is in flight towards a CTA that has left
+  cluster_wait();
+  if (warp == 2) pair_tmem_dealloc(tmem, 512);
 }
 
 // Dense, several queries per sequence: zeros behind each query's keys, and acc_out = acc + the weights
@@ -472,15 +552,14 @@ int launch_weights(const uint16_t* q, const WeightsParams& p, int64_t B, cudaStr
   const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
   CUtensorMap q_map, k_map;
   const uint64_t row = kDqk * 2;
-  if (!dsa_host::encode_tensor_map_2d(&q_map, dt, const_cast<uint16_t*>(q), kDqk, (uint64_t)p.BT * kHeads, row, 64, kHeads,
-                                      sw))
+  if (!dsa_host::encode_tensor_map_2d(&q_map, dt, const_cast<uint16_t*>(q), kDqk, (uint64_t)p.BT * kHeads, row, 64, 64, sw))
     return DSA_ERR_CUDA;
   k_map = q_map;
   if (!SELECTED) {
-    const uint64_t dims[3] = {(uint64_t)kDqk, (uint64_t)p.S_max, (uint64_t)B};
-    const uint64_t strides[2] = {row, row * (uint64_t)p.S_max};
-    const uint32_t box[3] = {64, kTile, 1};
-    if (!dsa_host::encode_tensor_map_3d(&k_map, dt, const_cast<uint16_t*>(p.kv), dims, strides, box, sw)) return DSA_ERR_CUDA;
+    // feature, row, block of 64 features, sequence: one box is two blocks of 128 rows, block by block
+    const uint64_t dims[4] = {64, (uint64_t)p.S_max, 9, (uint64_t)B}, strides[3] = {row, 128, row * (uint64_t)p.S_max};
+    const uint32_t box[4] = {64, kRows, 2, 1};
+    if (!dsa_host::encode_tensor_map(&k_map, dt, 4, const_cast<uint16_t*>(p.kv), dims, strides, box, sw)) return DSA_ERR_CUDA;
   }
   static uint64_t seen[dsa_host::kMaxSetupDevices];
   if (dsa_host::needs_setup(seen, nullptr)) {
@@ -496,9 +575,9 @@ int launch_weights(const uint16_t* q, const WeightsParams& p, int64_t B, cudaStr
     if (rc != DSA_OK) return rc;
   }
   const int64_t tiles = p.BT * (((SELECTED ? p.k : p.S_max) + kTile - 1) / kTile);
-  const unsigned grid = (unsigned)std::min<int64_t>(dsa_host::device_sm_count(), tiles);
-  const int rc = dsa_host::launch(mla_weights_kernel<SELECTED>, dim3(grid), dim3(SELECTED ? 512 : 384), kSmem, stream, q_map,
-                                  k_map, p);
+  const unsigned pairs = (unsigned)std::min<int64_t>(dsa_host::device_sm_count() / 2, tiles);
+  const int rc = dsa_host::launch_clusters(mla_weights_kernel<SELECTED>, 2, pairs, SELECTED ? 512 : 384, kSmem, stream, q_map,
+                                           k_map, p);
   if (rc != DSA_OK) return rc;
   if (p.T == 1) return DSA_OK;
   if (!SELECTED)
@@ -514,6 +593,7 @@ int launch_mla_weights(const uint16_t* q, const uint16_t* kv, const int32_t* idx
                        const int32_t* kv_len, int B, int T, int S_max, int k, float softmax_scale, float* w, int64_t ld,
                        const float* acc, float* acc_out, cudaStream_t stream, int* status) {
   WeightsParams p = {};
+  p.q = q;
   p.kv = kv;
   p.idx = idx;
   p.lse = lse;
