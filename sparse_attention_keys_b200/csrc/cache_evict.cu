@@ -7,10 +7,10 @@
 // kept row behind `keep` moves into the i-th row given up before it: sources and destinations never
 // overlap, the moves need no order, and the bytes moved are the fewest that leave a dense cache.
 //
-// select: a cluster of CTAs per sequence holds the rows' (weight, position) in shared memory where
-// they fit, and finds the border key by three histogram passes over an order-preserving 32-bit
-// image of the weight (11 + 11 + 10 bits), the CTAs reading one another's histograms through
-// distributed shared memory; a last pass breaks ties by row and lists movers and holes in order.
+// select: a cluster of CTAs per sequence holds the rows in registers where they fit, 16 to a thread, each as
+// an order-preserving 32-bit image of its weight and bits of masks that say what it is, and finds the
+// border key by three histogram passes (11 + 11 + 10 bits), the CTAs reading one another's histograms
+// through distributed shared memory; a last pass breaks ties by row and lists movers and holes in order.
 // move: a warp per two moved rows. Bound: the n (weight, position) pairs once, and HBM for the moves. 64
 // sequences of 12000 to 16384 rows cut to 8192 (about 550 MB): select 23 us, move 95 us, 4.6 TB/s in all; one
 // sequence of 131072 cut to 8191: 34 us, most of it the select's barriers and passes.
@@ -26,7 +26,10 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kCachedRows = 16384;       // rows per CTA kept in shared memory (8 bytes each)
+constexpr int kFine = 8;                 // bins of a histogram that make a coarse one
+constexpr int kCoarse = kBins / kFine;
+constexpr int kCachedGroups = 16;        // groups of 32 rows that a warp holds, a row of each per lane
+constexpr int kCachedRows = kCachedGroups * kThreads;
 constexpr int kMaxCluster = 8;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -38,13 +41,6 @@ __device__ __forceinline__ uint32_t ld_cluster(const void* p, uint32_t rank) {
   uint32_t a, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 ld_cluster_2(const void* p, uint32_t rank) {
-  uint32_t a;
-  uint2 v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -77,14 +73,14 @@ struct EvictParams {
   float* k_scale;
 };
 
-// CACHED: the rows of a CTA fit into shared memory.
+// CACHED: the rows of a CTA fit into its registers; otherwise every pass reads them again, a chunk at a time.
 template <bool CACHED>
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictParams p) {
-  extern __shared__ __align__(16) uint32_t rows_sm[];        // [per][2]: weight bits, position
+  constexpr int kGroups = CACHED ? kCachedGroups : 4;        // that a warp holds at a time
   __shared__ __align__(16) uint32_t hist[2][kBins];                        // ordinary and protected rows
+  __shared__ __align__(16) uint32_t coarse[2][kCoarse], all_sm[kCoarse];   // of this CTA's histograms, of all CTAs' together
   __shared__ uint32_t cnt_sm[8];                             // this CTA's words that the others read (kNewest ...)
   __shared__ uint32_t warp_sm[kWarps];
-  __shared__ uint32_t found_sm[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int b = blockIdx.x / p.C;
@@ -132,11 +128,36 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     return __reduce_add_sync(0xffffffffu, v);
   };
   for (int i = tid; i < 2 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+  // A warp's run of rows [w0, w1) comes in chunks of kGroups groups; lane i holds row `at + 32 * it + i` of
+  // the chunk's group `it`, and bit `it` of a lane's masks is that row's.
+  const int w0 = min(r1, r0 + warp * per_warp), w1 = min(r1, w0 + per_warp);
+  uint32_t key[kGroups];
+  int ps[kGroups];
+  uint32_t valid = 0, safe_rows = 0;                          // rows there are, protected ones
+  // the bits of the lane's rows below `end`
+  auto below = [&](int at, int end) {
+    return (1u << max(0, min(kGroups, (int)(((int64_t)end - at - lane + 31) >> 5)))) - 1u;
+  };
+  int groups = 0;                                             // of the chunk
+  auto load = [&](int at) {
+    valid = below(at, w1);
+    groups = (w1 - at + 31) >> 5;
+#pragma unroll
+    for (int it = 0; it < kGroups && it < groups; ++it) {
+      if (!((valid >> it) & 1u)) continue;
+      key[it] = __float_as_uint(acc[at + 32 * it + lane]);
+      ps[it] = pos[at + 32 * it + lane];
+    }
+#pragma unroll
+    for (int it = 0; it < kGroups && it < groups; ++it)
+      if ((valid >> it) & 1u) key[it] = weight_key(__uint_as_float(key[it]));
+  };
   int newest = INT32_MIN;
-  for (int r = r0 + tid; r < r1; r += kThreads) {
-    const int ps = pos[r];
-    if (CACHED) *reinterpret_cast<uint2*>(rows_sm + 2 * (r - r0)) = make_uint2(__float_as_uint(acc[r]), (uint32_t)ps);
-    newest = max(newest, ps);
+  for (int at = w0; at < w1; at += 32 * kGroups) {
+    load(at);
+#pragma unroll
+    for (int it = 0; it < kGroups && it < groups; ++it)
+      if ((valid >> it) & 1u) newest = max(newest, ps[it]);
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) newest = max(newest, __shfl_xor_sync(0xffffffffu, newest, d));
@@ -157,25 +178,64 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   const int64_t from = (int64_t)newest - p.recent;
   const int recent_from = (int)max(from, (int64_t)INT32_MIN);
   auto protects = [&](int ps) { return ps > recent_from || ps < p.sinks || from < INT32_MIN; };
-  // A row's key and class; shared memory holds (weight, position) until the next loop, then these.
-  auto row_of = [&](int r) {
-    return CACHED ? *reinterpret_cast<const uint2*>(rows_sm + 2 * (r - r0))
-                  : make_uint2(weight_key(acc[r]), protects(pos[r]) ? 1u : 0u);
+  auto classify = [&]() {
+    safe_rows = 0;
+#pragma unroll
+    for (int it = 0; it < kGroups && it < groups; ++it)
+      if (((valid >> it) & 1u) && protects(ps[it])) safe_rows |= 1u << it;
+  };
+  // f(at) for every chunk of the warp's run, its rows in registers
+  auto each_chunk = [&](auto f) {
+    if (CACHED) {
+      f(w0);
+    } else {
+      for (int at = w0; at < w1; at += 32 * kGroups) {
+        load(at);
+        classify();
+        f(at);
+      }
+    }
+  };
+  if (CACHED) classify();
+  // The state of every row below the budget, as if all of them stayed: a given-up one's is written again when its
+  // successor moves there. (Copying only those that stay, after the selection, took 7000 cycles more.)
+  const int step = p.C * kThreads;
+  for (int r = (int)rank * kThreads + tid; r < p.keep; r += 4 * step) {
+    float a[4];
+    int q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (copy_acc && r + i * step < p.keep) a[i] = acc[r + i * step];
+      if (copy_pos && r + i * step < p.keep) q[i] = pos[r + i * step];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (r + i * step >= p.keep) break;
+      if (copy_acc) acc_out[r + i * step] = a[i];
+      if (copy_pos) pos_out[r + i * step] = q[i];
+      if (src) src[r + i * step] = r + i * step;
+    }
+  }
+
+  // The coarse bins of this CTA's histogram `which`, once it is complete.
+  auto sum_bins = [&](int which, int i) {
+    const uint4* h = reinterpret_cast<const uint4*>(&hist[which][kFine * i]);
+    const uint4 x = h[0], y = h[1];
+    coarse[which][i] = ((x.x + x.y) + (x.z + x.w)) + ((y.x + y.y) + (y.z + y.w));
   };
 
   // first digit, for both classes
   uint32_t safe = 0;
-  for (int r = r0 + tid; r < r1; r += kThreads) {
-    const uint2 row = CACHED ? *reinterpret_cast<const uint2*>(rows_sm + 2 * (r - r0))
-                               : make_uint2(__float_as_uint(acc[r]), (uint32_t)pos[r]);
-    const uint32_t key = weight_key(__uint_as_float(row.x));
-    const bool yes = protects((int)row.y);
-    if (CACHED) *reinterpret_cast<uint2*>(rows_sm + 2 * (r - r0)) = make_uint2(key, yes ? 1u : 0u);
-    safe += yes;
-    atomicAdd(&hist[yes ? 1 : 0][key >> 21], 1u);
-  }
+  each_chunk([&](int) {
+    safe += __popc(safe_rows);
+#pragma unroll
+    for (int it = 0; it < kGroups && it < groups; ++it)
+      if ((valid >> it) & 1u) atomicAdd(&hist[(safe_rows >> it) & 1u][key[it] >> 21], 1u);
+  });
   safe = __reduce_add_sync(0xffffffffu, safe);
   if (lane == 0 && safe) atomicAdd(&cnt_sm[kSafe], safe);
+  __syncthreads();
+  if (tid < 2 * kCoarse) sum_bins(tid / kCoarse, tid % kCoarse);
   sync_all();
   // exclusive sum over the block's threads of v, and the total
   auto block_scan = [&](uint32_t v, uint32_t& total) {
@@ -199,35 +259,63 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     return (warp ? base : 0u) + s - v;
   };
   // The bin of histogram `which` in which the want-th largest key lies; `want` becomes its rank among the
-  // bin's keys. Every CTA adds up all histograms for itself, two bins a thread: that costs one cluster
-  // barrier a digit (sharing the bins out moves less, but took two more barriers and twice the time).
+  // bin's keys. The CTAs' coarse bins are added up first, then only the eight bins of the one it is in, by every
+  // warp for itself. (Adding up all 2048 bins of eight CTAs took 4500 cycles a digit, most of it remote reads.)
   auto find_bin = [&](int which, uint32_t& want) {
-    uint32_t h0 = 0, h1 = 0, total;
-    if (p.C == 1) {
-      h0 = hist[which][2 * tid];
-      h1 = hist[which][2 * tid + 1];
-    } else {
-      uint2 h[kMaxCluster];
+    if (tid < kCoarse) {
+      uint32_t h = 0;
 #pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) h[c] = c < p.C ? ld_cluster_2(&hist[which][2 * tid], (uint32_t)c) : make_uint2(0, 0);
-#pragma unroll
-      for (int c = 0; c < kMaxCluster; ++c) {
-        h0 += h[c].x;
-        h1 += h[c].y;
-      }
-    }
-    const uint32_t before = block_scan(h0 + h1, total);       // keys in lower bins
-    const uint32_t up1 = total - before - h0 - h1, up0 = up1 + h1;     // keys in bins above
-    if (want > up1 && want <= up1 + h1) {
-      found_sm[0] = 2 * tid + 1;
-      found_sm[1] = up1;
-    } else if (want > up0 && want <= up0 + h0) {
-      found_sm[0] = 2 * tid;
-      found_sm[1] = up0;
+      for (int c = 0; c < kMaxCluster; ++c)
+        if (c < p.C) h += ld_cluster(&coarse[which][tid], (uint32_t)c);
+      all_sm[tid] = h;
     }
     __syncthreads();
-    want -= found_sm[1];
-    return found_sm[0];
+    // lane i: coarse bins [8 i, 8 i + 8), and how many keys lie in those above
+    const uint4* h = reinterpret_cast<const uint4*>(&all_sm[8 * lane]);
+    const uint4 x = h[0], y = h[1];
+    const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    uint32_t up = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) up += v[i];
+    const uint32_t own = up;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t o = __shfl_down_sync(0xffffffffu, up, d);
+      if (lane + d < 32) up += o;
+    }
+    up -= own;
+    uint32_t bin = 0, above = 0;
+    const bool here = want > up && want <= up + own;
+    if (here) {
+      above = up;
+      bin = 7;
+#pragma unroll
+      for (int i = 7; i > 0; --i)
+        if ((int)bin == i && want > above + v[i]) {
+          above += v[i];
+          bin = i - 1;
+        }
+      bin += 8 * lane;
+    }
+    const int where = __ffs(__ballot_sync(0xffffffffu, here)) - 1;       // the histogram holds at least `want` keys
+    bin = __shfl_sync(0xffffffffu, bin, where);
+    want -= __shfl_sync(0xffffffffu, above, where);
+    // the eight bins of it: lane i adds up bin i % 8 of the CTAs i / 8 and i / 8 + 4
+    uint32_t f = 0;
+    const uint32_t* fine = &hist[which][kFine * bin + (lane & 7)];
+    if (lane >> 3 < p.C) f = ld_cluster(fine, (uint32_t)lane >> 3);
+    if ((lane >> 3) + 4 < p.C) f += ld_cluster(fine, ((uint32_t)lane >> 3) + 4);
+    f += __shfl_xor_sync(0xffffffffu, f, 8);
+    f += __shfl_xor_sync(0xffffffffu, f, 16);
+    uint32_t over = f;                                        // keys in this bin and those of the eight above it
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) {
+      const uint32_t o = __shfl_down_sync(0xffffffffu, over, d, 8);
+      if ((lane & 7) + d < 8) over += o;
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, want > over - f && want <= over)) - 1;
+    want -= __shfl_sync(0xffffffffu, over - f, at);
+    return kFine * bin + (uint32_t)(at & 7);
   };
   uint32_t unused0, unused1;
   const uint32_t safe_total = gather(kSafe, unused0, unused1);
@@ -242,55 +330,69 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
     const uint32_t mask = digit == 1 ? 0xffe00000u : 0xfffffc00u;
     hist[which][2 * tid] = hist[which][2 * tid + 1] = 0;
     __syncthreads();
-    for (int r = r0 + tid; r < r1; r += kThreads) {
-      const uint2 row = row_of(r);
-      if ((row.x & mask) == prefix && row.y == cls)
-        atomicAdd(&hist[which][(row.x >> shift) & (digit == 1 ? 2047u : 1023u)], 1u);
-    }
+    each_chunk([&](int) {
+      const uint32_t rows = valid & (cls ? safe_rows : ~safe_rows);
+#pragma unroll
+      for (int it = 0; it < kGroups && it < groups; ++it)
+        if (((rows >> it) & 1u) && (key[it] & mask) == prefix)
+          atomicAdd(&hist[which][(key[it] >> shift) & (digit == 1 ? 2047u : 1023u)], 1u);
+    });
+    __syncthreads();
+    if (tid < kCoarse) sum_bins(which, tid);
     sync_all();
     prefix |= find_bin(which, want) << shift;
   }
-  // The border key is `prefix`; `want` rows of the class on it are kept, the lowest ones.
-  // 0: given up, 1: kept, 2: kept if among the first `want` on the border
-  auto judge = [&](int r) {
-    const uint2 row = row_of(r);
-    return row.y != cls ? (int)row.y : (row.x > prefix ? 1 : (row.x == prefix ? 2 : 0));
-  };
-  // rows on the border in this warp's run, then before it in the sequence
-  const int w0 = min(r1, r0 + warp * per_warp), w1 = min(r1, w0 + per_warp);
-  auto exclusive = [&](uint32_t mine, int slot) {             // over the cluster's warps, row order
-    uint32_t total, before, behind;
-    const uint32_t base = block_scan(lane == 0 ? mine : 0u, total);
-    if (tid == 0) cnt_sm[slot] = total;
-    sync_all();
-    gather(slot, before, behind);
-    return before + __shfl_sync(0xffffffffu, base, 0);
-  };
-  // two bits a row keep the judgement of the first 16 groups of a warp's run
-  uint32_t codes = 0, ties = 0;
-  auto code = [&](int it, int r) { return it < 16 ? (int)((codes >> (2 * it)) & 3u) : (r < w1 ? judge(r) : 0); };
-  for (int r = w0 + lane, it = 0; r - lane < w1; r += 32, ++it) {
-    const int j = r < w1 ? judge(r) : 0;
-    if (it < 16) codes |= (uint32_t)j << (2 * it);
-    ties += __popc(__ballot_sync(0xffffffffu, j == 2));
-  }
-  const uint32_t ties_before = exclusive(ties, kTies);
-  // holes (given up, below the budget) and movers (kept, behind it): counted, then listed in row order
-  const uint32_t lower = (1u << lane) - 1u;
-  uint32_t holes = 0, movers = 0;
-  {
-    uint32_t t = ties_before;
-    for (int r = w0 + lane, it = 0; r - lane < w1; r += 32, ++it) {
-      const int j = code(it, r);
-      const uint32_t eq = __ballot_sync(0xffffffffu, j == 2);
-      const bool kept = j == 1 || (j == 2 && t + __popc(eq & lower) < want);
-      t += __popc(eq);
-      holes += __popc(__ballot_sync(0xffffffffu, r < w1 && !kept && r < p.keep));
-      movers += __popc(__ballot_sync(0xffffffffu, kept && r >= p.keep));
+  // The border key is `prefix`; `want` rows of the class on it are kept, the lowest ones. Rows kept whatever
+  // the ties, and those on the border:
+  auto judge = [&](uint32_t& kept, uint32_t& border) {
+    const uint32_t rows = valid & (cls ? safe_rows : ~safe_rows);
+    kept = cls ? 0u : safe_rows;
+    border = 0;
+#pragma unroll
+    for (int it = 0; it < kGroups && it < groups; ++it) {
+      if (!((rows >> it) & 1u)) continue;
+      if (key[it] > prefix) kept |= 1u << it;
+      if (key[it] == prefix) border |= 1u << it;
     }
-  }
+  };
+  uint32_t kept = 0, border = 0, ties = 0, total, before, behind;
+  each_chunk([&](int) {
+    judge(kept, border);
+    ties += __popc(border);
+  });
+  // rows on the border in this warp's run, then before it in the sequence
+  ties = __reduce_add_sync(0xffffffffu, ties);
+  const uint32_t tie_base = block_scan(lane == 0 ? ties : 0u, total);
+  if (tid == 0) cnt_sm[kTies] = total;
+  sync_all();
+  const uint32_t all_ties = gather(kTies, before, behind);
+  const uint32_t ties_before = before + __shfl_sync(0xffffffffu, tie_base, 0);
+  const uint32_t lower = (1u << lane) - 1u;
+  // the chunk's kept rows; t: rows on the border before it
+  auto settle = [&](uint32_t& t) {
+    if (!CACHED) judge(kept, border);
+    if (all_ties == want) {
+      kept |= border;
+      return;
+    }
+#pragma unroll
+    for (int it = 0; it < kGroups && it < groups; ++it) {
+      const uint32_t eq = __ballot_sync(0xffffffffu, (border >> it) & 1u);
+      if (((border >> it) & 1u) && t + __popc(eq & lower) < want) kept |= 1u << it;
+      t += __popc(eq);
+    }
+  };
+  // Holes (given up, below the budget) and movers (kept, behind it): counted, then listed in row order.
+  uint32_t holes = 0, movers = 0, t = ties_before;
+  each_chunk([&](int at) {
+    settle(t);
+    const uint32_t low = below(at, p.keep);
+    holes += __popc(valid & ~kept & low);
+    movers += __popc(kept & ~low);
+  });
+  holes = __reduce_add_sync(0xffffffffu, holes);
+  movers = __reduce_add_sync(0xffffffffu, movers);
   // both in one barrier: a CTA's counts are at most its rows
-  uint32_t total, behind;
   const uint32_t hole_base = block_scan(lane == 0 ? holes : 0u, total);
   if (tid == 0) cnt_sm[kHoles] = total;
   const uint32_t mover_base = block_scan(lane == 0 ? movers : 0u, total);
@@ -300,43 +402,25 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   gather(kMovers, movers, behind);
   holes += __shfl_sync(0xffffffffu, hole_base, 0);
   movers += __shfl_sync(0xffffffffu, mover_base, 0);
-  // the state of rows that stay is read four groups ahead of the walk that needs it
-  float a4[4];
-  int p4[4];
-  auto fetch = [&](int r) {
+  t = ties_before;
+  each_chunk([&](int at) {
+    if (!CACHED) settle(t);
+    const uint32_t low = below(at, p.keep), hole = valid & ~kept & low, mover = kept & ~low;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int at = r + 32 * k;
-      if (at < w1 && at < p.keep) {
-        if (copy_acc) a4[k] = acc[at];
-        if (copy_pos) p4[k] = pos[at];
+    for (int it = 0; it < kGroups && it < groups; ++it) {
+      const int first = at + 32 * it;
+      if (first < p.keep) {
+        const uint32_t hb = __ballot_sync(0xffffffffu, (hole >> it) & 1u);
+        if ((hole >> it) & 1u) moves[1 + p.L + holes + __popc(hb & lower)] = first + lane;
+        holes += __popc(hb);
+      }
+      if (first + 31 >= p.keep) {
+        const uint32_t mb = __ballot_sync(0xffffffffu, (mover >> it) & 1u);
+        if ((mover >> it) & 1u) moves[1 + movers + __popc(mb & lower)] = first + lane;
+        movers += __popc(mb);
       }
     }
-  };
-  uint32_t t = ties_before;
-  for (int r4 = w0 + lane, it4 = 0; r4 - lane < w1; r4 += 128, it4 += 4) {
-    fetch(r4);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int r = r4 + 32 * k;
-      if (r - lane >= w1) break;
-      const int j = code(it4 + k, r);
-      const uint32_t eq = __ballot_sync(0xffffffffu, j == 2);
-      const bool kept = j == 1 || (j == 2 && t + __popc(eq & lower) < want);
-      t += __popc(eq);
-      const bool hole = r < w1 && !kept && r < p.keep, mover = kept && r >= p.keep;
-      const uint32_t hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
-      if (hole) moves[1 + p.L + holes + __popc(hb & lower)] = r;
-      if (mover) moves[1 + movers + __popc(mb & lower)] = r;
-      if (kept && r < p.keep) {
-        if (copy_acc) acc_out[r] = a4[k];
-        if (copy_pos) pos_out[r] = p4[k];
-        if (src) src[r] = r;
-      }
-      holes += __popc(hb);
-      movers += __popc(mb);
-    }
-  }
+  });
   if (rank == 0 && tid == 0) {
     p.len_out[b] = p.keep;
     moves[0] = (int)all_holes;                                 // as many holes as movers
@@ -427,17 +511,9 @@ int launch_cache_evict(const float* acc, const int32_t* pos, const int32_t* kv_l
   p.C = C;
   const int64_t per_warp = (((int64_t)S_max + C * kWarps - 1) / (C * kWarps) + 31) / 32 * 32;
   const bool cached = per_warp * kWarps <= kCachedRows;
-  const size_t smem = cached ? (size_t)per_warp * kWarps * 8 : 0;
-  static uint64_t seen[dsa_host::kMaxSetupDevices];
-  if (dsa_host::needs_setup(seen, nullptr)) {
-    if (cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCachedRows * 8) != cudaSuccess)
-      return DSA_ERR_CUDA;
-    dsa_host::mark_setup(seen);
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(B * C));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
