@@ -12,8 +12,8 @@
 // border key by three histogram passes (11 + 11 + 10 bits), the CTAs reading one another's histograms
 // through distributed shared memory; a last pass breaks ties by row and lists movers and holes in order.
 // move: a warp per two moved rows. Bound: the n (weight, position) pairs once, and HBM for the moves. 64
-// sequences of 12000 to 16384 rows cut to 8192 (about 550 MB): select 23 us, move 95 us, 4.6 TB/s in all; one
-// sequence of 131072 cut to 8191: 34 us, most of it the select's barriers and passes.
+// sequences of 12000 to 16384 rows cut to 8192 (about 550 MB): select 20 us, move 95 us, 4.8 TB/s in all; one
+// sequence of 131072 cut to 8191: 25 us, most of it the select's barriers and passes.
 #include <algorithm>
 
 #include "common.cuh"
@@ -78,9 +78,9 @@ template <bool CACHED>
 __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictParams p) {
   constexpr int kGroups = CACHED ? kCachedGroups : 4;        // that a warp holds at a time
   __shared__ __align__(16) uint32_t hist[2][kBins];                        // ordinary and protected rows
-  __shared__ __align__(16) uint32_t coarse[2][kCoarse], all_sm[kCoarse];   // of this CTA's histograms, of all CTAs' together
+  __shared__ __align__(16) uint32_t coarse[2][kCoarse], all_sm[kCoarse];   // of this CTA's histograms, of all CTAs'
   __shared__ uint32_t cnt_sm[8];                             // this CTA's words that the others read (kNewest ...)
-  __shared__ uint32_t warp_sm[kWarps];
+  __shared__ uint32_t warp_sm[kWarps], scan_sm[3][kWarps], found_sm[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int b = blockIdx.x / p.C;
@@ -237,30 +237,22 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   __syncthreads();
   if (tid < 2 * kCoarse) sum_bins(tid / kCoarse, tid % kCoarse);
   sync_all();
-  // exclusive sum over the block's threads of v, and the total
-  auto block_scan = [&](uint32_t v, uint32_t& total) {
-    uint32_t s = v;
+  // the warps' words of scan_sm[slot] summed over the warps before this one, and over all of the block
+  auto scan_warps = [&](int slot, uint32_t& total) {
+    uint32_t s = scan_sm[slot][lane];
+    const uint32_t v = s;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t o = __shfl_up_sync(0xffffffffu, s, d);
       if (lane >= d) s += o;
     }
-    __syncthreads();
-    if (lane == 31) warp_sm[warp] = s;
-    __syncthreads();
-    uint32_t ws = warp_sm[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, ws, d);
-      if (lane >= d) ws += o;
-    }
-    total = __shfl_sync(0xffffffffu, ws, 31);
-    const uint32_t base = __shfl_sync(0xffffffffu, ws, warp ? warp - 1 : 0);
-    return (warp ? base : 0u) + s - v;
+    total = __shfl_sync(0xffffffffu, s, 31);
+    return __shfl_sync(0xffffffffu, s - v, warp);
   };
   // The bin of histogram `which` in which the want-th largest key lies; `want` becomes its rank among the
-  // bin's keys. The CTAs' coarse bins are added up first, then only the eight bins of the one it is in, by every
-  // warp for itself. (Adding up all 2048 bins of eight CTAs took 4500 cycles a digit, most of it remote reads.)
+  // bin's keys. The CTAs' coarse bins are added up first, then one warp finds the bin among the eight of the one
+  // it is in. (Adding up all 2048 bins of eight CTAs took 4500 cycles a digit, most of it remote reads; every
+  // warp finding the bin for itself, 1000 more than the barrier.)
   auto find_bin = [&](int which, uint32_t& want) {
     if (tid < kCoarse) {
       uint32_t h = 0;
@@ -270,52 +262,60 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
       all_sm[tid] = h;
     }
     __syncthreads();
-    // lane i: coarse bins [8 i, 8 i + 8), and how many keys lie in those above
-    const uint4* h = reinterpret_cast<const uint4*>(&all_sm[8 * lane]);
-    const uint4 x = h[0], y = h[1];
-    const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-    uint32_t up = 0;
+    if (warp == 0) {
+      // lane i: coarse bins [8 i, 8 i + 8), and how many keys lie in those above
+      const uint4* h = reinterpret_cast<const uint4*>(&all_sm[8 * lane]);
+      const uint4 x = h[0], y = h[1];
+      const uint32_t v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      uint32_t up = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) up += v[i];
-    const uint32_t own = up;
+      for (int i = 0; i < 8; ++i) up += v[i];
+      const uint32_t own = up;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t o = __shfl_down_sync(0xffffffffu, up, d);
-      if (lane + d < 32) up += o;
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_down_sync(0xffffffffu, up, d);
+        if (lane + d < 32) up += o;
+      }
+      up -= own;
+      uint32_t bin = 0, above = 0;
+      const bool here = want > up && want <= up + own;
+      if (here) {
+        above = up;
+        bin = 7;
+#pragma unroll
+        for (int i = 7; i > 0; --i)
+          if ((int)bin == i && want > above + v[i]) {
+            above += v[i];
+            bin = i - 1;
+          }
+        bin += 8 * lane;
+      }
+      const int where = __ffs(__ballot_sync(0xffffffffu, here)) - 1;       // the histogram holds at least `want` keys
+      bin = __shfl_sync(0xffffffffu, bin, where);
+      const uint32_t in = want - __shfl_sync(0xffffffffu, above, where);
+      // the eight bins of it: lane i adds up bin i % 8 of the CTAs i / 8 and i / 8 + 4
+      uint32_t f = 0;
+      const uint32_t* fine = &hist[which][kFine * bin + (lane & 7)];
+      if (lane >> 3 < p.C) f = ld_cluster(fine, (uint32_t)lane >> 3);
+      if ((lane >> 3) + 4 < p.C) f += ld_cluster(fine, ((uint32_t)lane >> 3) + 4);
+      f += __shfl_xor_sync(0xffffffffu, f, 8);
+      f += __shfl_xor_sync(0xffffffffu, f, 16);
+      uint32_t over = f;                                        // keys in this bin and those of the eight above it
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) {
+        const uint32_t o = __shfl_down_sync(0xffffffffu, over, d, 8);
+        if ((lane & 7) + d < 8) over += o;
+      }
+      const int at = __ffs(__ballot_sync(0xffffffffu, in > over - f && in <= over)) - 1;
+      const uint32_t rank_in = in - __shfl_sync(0xffffffffu, over - f, at);
+      if (lane == 0) {
+        found_sm[0] = kFine * bin + (uint32_t)(at & 7);
+        found_sm[1] = rank_in;
+      }
     }
-    up -= own;
-    uint32_t bin = 0, above = 0;
-    const bool here = want > up && want <= up + own;
-    if (here) {
-      above = up;
-      bin = 7;
-#pragma unroll
-      for (int i = 7; i > 0; --i)
-        if ((int)bin == i && want > above + v[i]) {
-          above += v[i];
-          bin = i - 1;
-        }
-      bin += 8 * lane;
-    }
-    const int where = __ffs(__ballot_sync(0xffffffffu, here)) - 1;       // the histogram holds at least `want` keys
-    bin = __shfl_sync(0xffffffffu, bin, where);
-    want -= __shfl_sync(0xffffffffu, above, where);
-    // the eight bins of it: lane i adds up bin i % 8 of the CTAs i / 8 and i / 8 + 4
-    uint32_t f = 0;
-    const uint32_t* fine = &hist[which][kFine * bin + (lane & 7)];
-    if (lane >> 3 < p.C) f = ld_cluster(fine, (uint32_t)lane >> 3);
-    if ((lane >> 3) + 4 < p.C) f += ld_cluster(fine, ((uint32_t)lane >> 3) + 4);
-    f += __shfl_xor_sync(0xffffffffu, f, 8);
-    f += __shfl_xor_sync(0xffffffffu, f, 16);
-    uint32_t over = f;                                        // keys in this bin and those of the eight above it
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) {
-      const uint32_t o = __shfl_down_sync(0xffffffffu, over, d, 8);
-      if ((lane & 7) + d < 8) over += o;
-    }
-    const int at = __ffs(__ballot_sync(0xffffffffu, want > over - f && want <= over)) - 1;
-    want -= __shfl_sync(0xffffffffu, over - f, at);
-    return kFine * bin + (uint32_t)(at & 7);
+    __syncthreads();
+    want = found_sm[1];
+    return found_sm[0];
   };
   uint32_t unused0, unused1;
   const uint32_t safe_total = gather(kSafe, unused0, unused1);
@@ -362,11 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   });
   // rows on the border in this warp's run, then before it in the sequence
   ties = __reduce_add_sync(0xffffffffu, ties);
-  const uint32_t tie_base = block_scan(lane == 0 ? ties : 0u, total);
+  if (lane == 0) scan_sm[0][warp] = ties;
+  __syncthreads();
+  const uint32_t tie_base = scan_warps(0, total);
   if (tid == 0) cnt_sm[kTies] = total;
   sync_all();
   const uint32_t all_ties = gather(kTies, before, behind);
-  const uint32_t ties_before = before + __shfl_sync(0xffffffffu, tie_base, 0);
+  const uint32_t ties_before = before + tie_base;
   const uint32_t lower = (1u << lane) - 1u;
   // the chunk's kept rows; t: rows on the border before it
   auto settle = [&](uint32_t& t) {
@@ -393,15 +395,20 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
   holes = __reduce_add_sync(0xffffffffu, holes);
   movers = __reduce_add_sync(0xffffffffu, movers);
   // both in one barrier: a CTA's counts are at most its rows
-  const uint32_t hole_base = block_scan(lane == 0 ? holes : 0u, total);
+  if (lane == 0) {
+    scan_sm[1][warp] = holes;
+    scan_sm[2][warp] = movers;
+  }
+  __syncthreads();
+  const uint32_t hole_base = scan_warps(1, total);
   if (tid == 0) cnt_sm[kHoles] = total;
-  const uint32_t mover_base = block_scan(lane == 0 ? movers : 0u, total);
+  const uint32_t mover_base = scan_warps(2, total);
   if (tid == 0) cnt_sm[kMovers] = total;
   sync_all();
   const uint32_t all_holes = gather(kHoles, holes, behind);
   gather(kMovers, movers, behind);
-  holes += __shfl_sync(0xffffffffu, hole_base, 0);
-  movers += __shfl_sync(0xffffffffu, mover_base, 0);
+  holes += hole_base;
+  movers += mover_base;
   t = ties_before;
   each_chunk([&](int at) {
     if (!CACHED) settle(t);
