@@ -7,22 +7,23 @@
 // The scores are computed transposed, S^T = K Q^T, so that a TMEM lane holds one key and the 128
 // columns its heads: the sum over the heads stays inside a thread pair. A CTA pair (cta_group::2, M = 256
 // keys, 128 per CTA) takes an equal share of all (query, 256-key tile) pairs; each CTA keeps 64 heads of
-// the query in shared memory (72 KB) while 32 KB slots of its keys (128 keys x 128 features) pass through a
-// ring of four. Per tile: 36 MMAs of 256 x 128 x 16 (65 cycles each, 2340) and 128 x 128 exponentials per
+// the query in shared memory (72 KB) while 48 KB slots of its keys (128 keys x 192 features) pass through a
+// ring of three. Per tile: 36 MMAs of 256 x 128 x 16 (65 cycles each, 2340) and 128 x 128 exponentials per
 // CTA (1024 cycles of MUFU). For one query per sequence HBM is the bound: a CTA's 147 KB a tile take an SM's
-// share of it 6300 cycles, and the ring's 128 KB cover its latency (45 us for 64 queries over 2048 to 4096
-// rows each, 5.0 TB/s; a CTA alone, with all heads and an 80 KB ring, 47 us).
+// share of it 6300 cycles, and the ring's 144 KB cover its latency (48 to 50 us for 64 queries over 2048 to
+// 4096 rows each, 4.9 TB/s; with 128 KB in slots of 128 features, a tenth of them empty, 51 us).
 //
-// A tile's contraction is cut into four parts of 128, 128, 128 and 192 features, each with an accumulator
-// of 128 columns of its own, that are added in registers. The exponential turns an absolute error of the score
-// into a relative one of the weight, and the tensor core's rounding of the running fp32 sum, 36 times over
-// 576 features, was what the weights' error came from: 6.7e-6 of them with one accumulator, 1.7e-6 with four
-// (fp32 matrix products leave 2e-6). It costs 5% of the time.
+// A tile's contraction is cut into three parts of 192 features, a slot and an accumulator of 128 columns each, that
+// are added in registers. The exponential turns an absolute error of the score into a relative one of the
+// weight, and the tensor core's rounding of the running fp32 sum, 36 times over 576 features, was what the
+// weights' error came from: 6.7e-6 of them with one accumulator, 2.1e-6 with three (fp32 matrix products
+// leave 2e-6). The parts take the four accumulators of TMEM in turn, so that the first of a tile is
+// computed while the last one's are read.
 //
 // Selected rows are gathered by four warps with 16-byte cp.async into the swizzled operand layout,
-// 256 bytes of each row per slot; a fifth hands the slots that have landed to the leader. (Hinting whole rows
-// into L2 a tile ahead was slower, 46.5 against 43.5 us for 64 queries of 2048 rows; so was hinting the next
-// dense tile, 55 against 50 us.)
+// 384 bytes of each row per slot (64 queries of 2048 rows: 45 us, 48 with 256 bytes at a time, 58 with 128: the
+// shorter the pieces, the more of HBM's pages are opened); a fifth hands the slots that have landed to the
+// leader. (Hinting whole rows into L2 a tile ahead was slower; so was hinting the next dense tile.)
 #include <math.h>
 
 #include <algorithm>
@@ -39,16 +40,17 @@ constexpr int kRows = 128;                         // keys of a tile on each CTA
 constexpr int kTile = 2 * kRows;
 constexpr int kQBlock = 64 * 128;                  // 8 KB: 64 features of this CTA's 64 heads
 constexpr int kBlock = kRows * 128;                // 16 KB: 64 features of 128 keys
-constexpr int kSlot = 2 * kBlock;
-constexpr int kSlots = 4;
+constexpr int kParts = 3;                          // parts of a contraction, 192 features each: a ring slot
+constexpr int kSlot = 3 * kBlock;                  // 48 KB
+constexpr int kSlots = 3;
+constexpr int kAccs = 4;                           // accumulators of 128 columns, taken by the parts in turn
 constexpr int kOffRing = 9 * kQBlock;
 constexpr int kOffBar = kOffRing + kSlots * kSlot;
-constexpr int kOffLse = kOffBar + 256;             // [2][128] fp32
-constexpr int kOffSum = kOffLse + 2 * 128 * 4;     // [2][128] fp32
+constexpr int kOffLse = kOffBar + 256;             // [4][128] fp32
+constexpr int kOffSum = kOffLse + 4 * 128 * 4;     // [2][128] fp32
 constexpr int kOffScan = kOffSum + 2 * 128 * 4;    // set-up words
 constexpr int kSmem = 1024 + kOffScan + 256;
 static_assert(kOffRing % 1024 == 0 && kSmem <= 232448, "shared memory per CTA");
-constexpr int kParts = 4;                          // parts of a contraction, an accumulator of 128 columns each
 constexpr int kGatherWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -121,20 +123,17 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
     mla_weights_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                        const WeightsParams p) {
   constexpr int kThreads = SELECTED ? 512 : 384;
-  // Parts handed over at a time: two where the MMAs are the bound (250 dense queries over 4100 rows: 103 us, and
-  // 111 one by one), one where the gather is (64 queries of 2048 rows: 43.5 us, and 46 by twos).
-  constexpr int kJoint = SELECTED ? 1 : 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* full = bars;                 // leader [kSlots]: both CTAs' keys landed
   uint64_t* empty = full + kSlots;       // [kSlots] their MMAs are done
   uint64_t* gathered = empty + kSlots;   // [kSlots] this CTA's keys landed (selected rows)
-  uint64_t* acc_full = gathered + kSlots;  // [kParts / kJoint] parts of the scores ready
-  uint64_t* acc_empty = acc_full + kParts;  // leader [kParts / kJoint]: both CTAs have read them
-  uint64_t* q_full = acc_empty + kParts;   // leader: both halves of the query landed
+  uint64_t* acc_full = gathered + kSlots;  // [kAccs] a part of the scores ready
+  uint64_t* acc_empty = acc_full + kAccs;  // leader [kAccs]: both CTAs have read it
+  uint64_t* q_full = acc_empty + kAccs;    // leader: both halves of the query landed
   uint64_t* q_empty = q_full + 1;        // the run's MMAs are done
-  uint64_t* sum_full = q_empty + 1;      // [4] the second half of the heads is summed, per quadrant
+  uint64_t* sum_full = q_empty + 1;      // [2][4] the second half of the heads is summed, per quadrant
   float* lse_sh = reinterpret_cast<float*>(smem + kOffLse);
   float* sum_sh = reinterpret_cast<float*>(smem + kOffSum);
   long long* scan_sh = reinterpret_cast<long long*>(smem + kOffScan);       // [kThreads / 32]
@@ -151,11 +150,11 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
       mbar_init(&empty[s], 1);
       mbar_init(&gathered[s], kGatherWarps * 32);
     }
-    for (int i = 0; i < kParts; ++i) {
+    for (int i = 0; i < kAccs; ++i) {
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 16);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&sum_full[i], 1);
+    for (int i = 0; i < 8; ++i) mbar_init(&sum_full[i], 1);
     mbar_init(q_full, 2);
     mbar_init(q_empty, 1);
     fence_barrier_init();
@@ -258,12 +257,12 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
         if (SELECTED) continue;
         const int b = (int)(r.tok / p.T);
         for (int t = r.t0; ok && t < r.t1; ++t)
-          for (int f = 0; f < 9 && acquire(); f += 2, advance()) {
+          for (int part = 0; part < kParts && acquire(); ++part, advance()) {
             const uint32_t bar = cluster_addr(&full[slot], 0);
             const int row = t * kTile + rank * kRows;
             if (row < r.keys) {
-              arrive_expect_tx_cluster(bar, kSlot);            // there is no block 9: zeros
-              pair_load_4d(ring + slot * kSlot, &k_map, bar, 0, row, f, b);
+              arrive_expect_tx_cluster(bar, kSlot);
+              pair_load_4d(ring + slot * kSlot, &k_map, bar, 0, row, 3 * part, b);
             } else {
               arrive_cluster(bar);       // no key of the tile on this CTA: its scores are not used
             }
@@ -280,31 +279,30 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
       const uint32_t idesc = idesc_f32acc(1, 1, 256, kHeads, 0, 0);
       const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(smem)), k_desc = sdesc_kmajor_sw128(ring);
       int slot = 0, run = 0;
-      uint32_t ph = 0, g = 0;
+      uint32_t ph = 0, i = 0;               // parts issued
       bool ok = true;
       for (; ok && r.left > 0; r.next(p), ++run) {
         if (!mbar_wait(q_full, run & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_Q)) break;
         tc_fence_after();
         const int tiles = r.t1 - r.t0;
-        for (int t = 0; ok && t < tiles; ++t, ++g) {
+        for (int t = 0; ok && t < tiles; ++t) {
 #pragma unroll
-          for (int f = 0; f < 9; f += 2) {                     // a slot is a part; the last one adds to the fourth
-            const int part = f < 8 ? f / 2 : kParts - 1;
-            if (!ok || (f < 8 && part % kJoint == 0 && !mbar_wait(&acc_empty[part / kJoint], (g + 1) & 1, &abort_flag, p.status,
-                                                                  DSA_SITE_WEIGHTS_ACC)) ||
+          for (int part = 0; part < kParts; ++part) {
+            if (!ok || !mbar_wait(&acc_empty[i & 3], ((i >> 2) + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC) ||
                 !mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL)) {
               ok = false;
               break;
             }
             if (SELECTED) cluster_fence();                     // both CTAs' threads wrote this slot
             tc_fence_after();
-            const uint64_t a = k_desc + (uint64_t)(slot * (kSlot >> 4)), b = q_desc + (uint64_t)(f * (kQBlock >> 4));
+            const uint64_t a = k_desc + (uint64_t)(slot * (kSlot >> 4)), b = q_desc + (uint64_t)(3 * part * (kQBlock >> 4));
 #pragma unroll
-            for (int k = 0; k < (f < 8 ? 8 : 4); ++k)
-              pair_mma_ss(part * kHeads, a + 2 * (k & 3) + (k >> 2) * (kBlock >> 4), b + 2 * (k & 3) + (k >> 2) * (kQBlock >> 4),
-                          idesc, k > 0 || f == 8);
+            for (int k = 0; k < 12; ++k)
+              pair_mma_ss((i & 3) * kHeads, a + 2 * (k & 3) + (k >> 2) * (kBlock >> 4),
+                          b + 2 * (k & 3) + (k >> 2) * (kQBlock >> 4), idesc, k > 0);
             pair_commit(&empty[slot], 3);
-            if (f == 8 || (f < 6 && part % kJoint == kJoint - 1)) pair_commit(&acc_full[part / kJoint], 3);
+            pair_commit(&acc_full[i & 3], 3);
+            ++i;
             if (++slot == kSlots) {
               slot = 0;
               ph ^= 1;
@@ -320,7 +318,7 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
     uint32_t ph = 0;
     bool ok = true;
     for (; ok && r.left > 0; r.next(p))
-      for (int i = 0; ok && i < 5 * (r.t1 - r.t0); ++i) {
+      for (int i = 0; ok && i < kParts * (r.t1 - r.t0); ++i) {
         ok = __all_sync(0xffffffffu, mbar_wait(&gathered[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL));
         if (!ok) break;
         fence_proxy_async_smem();        // cp.async writes -> MMA reads
@@ -361,18 +359,18 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
       int row = row_of(r.t0);
       for (int t = r.t0; ok && t < r.t1; ++t) {
         const int next = row_of(t + 1);
-        for (int f = 0; f < 9 && acquire(); f += 2, advance()) {
+        for (int part = 0; part < kParts && acquire(); ++part, advance()) {
           const uint32_t dst = ring + slot * kSlot;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            // four rows per step, eight 16-byte chunks of each of two blocks; rows that take no part are zeros
+            // four rows per step, eight 16-byte chunks of each of three blocks; rows that take no part are zeros
             const int rr = 4 * i + (lane >> 3), c = lane & 7;
             const int src = __shfl_sync(0xffffffffu, row, rr);
             const int at = 32 * v + rr;
             const uint32_t to = dst + at * 128 + ((c ^ (at & 7)) << 4);
-            const uint16_t* from = kv + (int64_t)max(src, 0) * kDqk + 64 * f + 8 * c;
-            cp_async_16_zfill(to, from, src >= 0);
-            if (f < 8) cp_async_16_zfill(to + kBlock, from + 64, src >= 0);
+            const uint16_t* from = kv + (int64_t)max(src, 0) * kDqk + 192 * part + 8 * c;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) cp_async_16_zfill(to + j * kBlock, from + 64 * j, src >= 0);
           }
           cp_async_mbar_arrive(&gathered[slot]);
         }
@@ -386,13 +384,13 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
     // ------------------------------------------------------------------ exponentials, two threads per key, 64 heads each
     const int key = (tid - 128) & 127, half = (tid - 128) >> 7, quad = warp & 3;
     const uint32_t t_row = tmem + ((uint32_t)(quad * 32) << 16) + 64 * half;
-    uint32_t g = 0;
+    uint32_t g = 0, i = 0;               // tiles, parts
     int run = 0;
     bool ok = true;
     for (; ok && r.left > 0; r.next(p), ++run) {
-      // the run's lse in units of log 2 (the four warps of a half write the same values; a warp two runs ahead of
-      // another cannot be: every tile needs all warps' release of the one before)
-      float* ls = lse_sh + (run & 1) * kHeads + 64 * half;
+      // the run's lse in units of log 2 (the four warps of a half write the same values). A part needs every
+      // warp's release of the one four before it, so no warp gets more than two tiles ahead of another: four buffers.
+      float* ls = lse_sh + (run & 3) * kHeads + 64 * half;
       const float2 l2 = __ldg(reinterpret_cast<const float2*>(p.lse + r.tok * kHeads + 64 * half) + lane);
       __syncwarp();
       *reinterpret_cast<float2*>(ls + 2 * lane) = make_float2(l2.x * kLog2e, l2.y * kLog2e);
@@ -412,45 +410,42 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
         float z[64];
 #pragma unroll
         for (int part = 0; part < kParts; ++part) {
-          if (part % kJoint == 0) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&acc_full[part / kJoint], g & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC));
-            if (!ok) break;
-            tc_fence_after();
-          }
+          ok = ok && __all_sync(0xffffffffu, mbar_wait(&acc_full[i & 3], (i >> 2) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t x[32];
-            tmem_ld32(t_row + part * kHeads + 32 * c, x);
+            tmem_ld32(t_row + (i & 3) * kHeads + 32 * c, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              z[32 * c + i] = part == 0 ? __uint_as_float(x[i]) : z[32 * c + i] + __uint_as_float(x[i]);
+            for (int j = 0; j < 32; ++j)
+              z[32 * c + j] = part == 0 ? __uint_as_float(x[j]) : z[32 * c + j] + __uint_as_float(x[j]);
           }
-          if (part % kJoint == kJoint - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(cluster_addr(&acc_empty[part / kJoint], 0));
-          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(cluster_addr(&acc_empty[i & 3], 0));
+          ++i;
         }
         if (!ok) break;
         float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 l4 = *reinterpret_cast<const float4*>(ls + i);
-          s4[0] += exp2_approx(fmaf(z[i], p.scale_log2, -l4.x));
-          s4[1] += exp2_approx(fmaf(z[i + 1], p.scale_log2, -l4.y));
-          s4[2] += exp2_approx(fmaf(z[i + 2], p.scale_log2, -l4.z));
-          s4[3] += exp2_approx(fmaf(z[i + 3], p.scale_log2, -l4.w));
+        for (int j = 0; j < 64; j += 4) {
+          const float4 l4 = *reinterpret_cast<const float4*>(ls + j);
+          s4[0] += exp2_approx(fmaf(z[j], p.scale_log2, -l4.x));
+          s4[1] += exp2_approx(fmaf(z[j + 1], p.scale_log2, -l4.y));
+          s4[2] += exp2_approx(fmaf(z[j + 2], p.scale_log2, -l4.z));
+          s4[3] += exp2_approx(fmaf(z[j + 3], p.scale_log2, -l4.w));
         }
         float sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
         float* other = sum_sh + (g & 1) * kRows + key;
         if (half == 1) {
           *other = sum;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sum_full[quad]);
+          if (lane == 0) mbar_arrive(&sum_full[4 * (g & 1) + quad]);
           continue;
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&sum_full[quad], g & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&sum_full[4 * (g & 1) + quad], (g >> 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC))) {
           ok = false;
           break;
         }
@@ -556,9 +551,9 @@ int launch_weights(const uint16_t* q, const WeightsParams& p, int64_t B, cudaStr
     return DSA_ERR_CUDA;
   k_map = q_map;
   if (!SELECTED) {
-    // feature, row, block of 64 features, sequence: one box is two blocks of 128 rows, block by block
+    // feature, row, block of 64 features, sequence: one box is three blocks of 128 rows, block by block
     const uint64_t dims[4] = {64, (uint64_t)p.S_max, 9, (uint64_t)B}, strides[3] = {row, 128, row * (uint64_t)p.S_max};
-    const uint32_t box[4] = {64, kRows, 2, 1};
+    const uint32_t box[4] = {64, kRows, 3, 1};
     if (!dsa_host::encode_tensor_map(&k_map, dt, 4, const_cast<uint16_t*>(p.kv), dims, strides, box, sw)) return DSA_ERR_CUDA;
   }
   static uint64_t seen[dsa_host::kMaxSetupDevices];
