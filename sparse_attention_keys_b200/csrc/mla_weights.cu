@@ -21,8 +21,8 @@
 // computed while the last one's are read.
 //
 // Selected rows are gathered by four warps with 16-byte cp.async into the swizzled operand layout,
-// 384 bytes of each row per slot (64 queries of 2048 rows: 45 us, 48 with 256 bytes at a time, 58 with 128: the
-// shorter the pieces, the more of HBM's pages are opened); a fifth hands the slots that have landed to the
+// 384 bytes of each row per slot (64 queries of 2048 rows: 45 us, 48 with 256 bytes at a time, 58 with 128, since
+// shorter pieces open more of the pages of HBM for the same bytes); a fifth hands the slots that have landed to the
 // leader. (Hinting whole rows into L2 a tile ahead was slower; so was hinting the next dense tile.)
 #include <math.h>
 
