@@ -210,3 +210,21 @@ def test_refusals_on_the_device():
     for bad in (dict(recent=-1), dict(sinks=-1), dict(workspace=torch.empty(4, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(dsa.DsaError):
             dsa.dsa_cache_evict(**{**good, **bad})
+
+
+@gpu
+@pytest.mark.parametrize("B,S,keep", [(2, 5000, 1800), (1, 140000, 70001), (1, 140000, 9)])
+def test_ties_across_every_warp_and_part_of_the_state_in_place(B, S, keep):
+    """Equal weights everywhere, so that the lowest rows stay; and positions alone written elsewhere."""
+    acc = torch.full((B, S), 0.5, device="cuda")
+    acc[:, ::7] = 0.25
+    pos = torch.arange(S, device="cuda", dtype=torch.int32).flip(0).expand(B, S).contiguous()
+    kv_len = torch.full((B,), S, dtype=torch.int32, device="cuda")
+    want = [plan(a, p, S, keep, 3, 0) for a, p in zip(acc.tolist(), pos.tolist())]
+    rows = [torch.stack([t[b][w] for b, w in enumerate(want)]) for t in (acc, pos)]
+    before, pos_out = pos.clone(), torch.full_like(pos, -7)
+    _, _, n, src = dsa.dsa_cache_evict(acc, pos, kv_len, keep, recent=3, pos_out=pos_out)
+    assert src.tolist() == want and n.tolist() == [keep] * B
+    assert torch.equal(acc[:, :keep], rows[0]) and torch.equal(pos_out[:, :keep], rows[1])
+    assert torch.equal(pos, before) and bool((pos_out[:, keep:] == -7).all())
+    assert dsa.dsa_get_device_status() == 0

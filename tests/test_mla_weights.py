@@ -137,6 +137,29 @@ def test_weights(B, T, S):
 
 
 @gpu
+def test_a_new_query_every_tile():
+    """Many queries in a row for each pair of CTAs, one tile each, whose lse lie far apart."""
+    B, T, S = 2, 800, 60
+    q, kv, q_pos, kv_len = make(B, T, S, seed=9, lens=[S, S - 1])
+    q *= (0.25 * (1 + torch.arange(T, device="cuda") % 7)).to(q.dtype)[None, :, None, None]
+    q_pos.fill_(S)
+    rows = [[torch.arange(visible(q_pos, kv_len, S, b, t), device="cuda") for t in range(T)] for b in range(B)]
+    lse = lse_of(q, kv, rows)
+    w, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len)
+    idx = torch.arange(S, device="cuda", dtype=torch.int32).expand(B, T, S).contiguous()
+    idx[1, :, S - 1] = -1
+    ws, _ = dsa.dsa_mla_weights_selected(q, kv, idx, lse)
+    assert dsa.dsa_get_device_status() == 0
+    ref = reference(q, kv, lse, rows)
+    for b in range(B):
+        n = len(rows[b][0])
+        want, tol = (torch.stack([r[i] for r in ref[b]]) for i in (0, 1))
+        for got in (w, ws):
+            close(got[b, :, :n], want, tol)
+            assert bool((got[b, :, n:S] == 0).all())
+
+
+@gpu
 def test_hidden_rows_lengths_and_minus_infinity():
     lens = [0, 1, 128, 129, 256, 300, 77]
     q, kv, q_pos, kv_len = make(7, 2, 256, seed=2, lens=lens)
