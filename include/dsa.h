@@ -458,8 +458,9 @@ DSA_API int dsa_mla_weights_selected(const uint16_t* q, const uint16_t* kv, cons
  *   acc     fp32 [B][S_max]   collected weight of each row
  *   pos     int32 [B][S_max]  position of each row's token (a row keeps it wherever it moves)
  *   kv_len  int32 [B]         rows present, clamped to [0, S_max]
- *   keep    rows to keep, >= 1;  recent, sinks >= 0: rows whose position is among the `recent`
- *           newest (above the sequence's largest position - recent) or below `sinks` are protected
+ *   keep    rows to keep, >= 1; a budget above S_max, up to INT_MAX, gives up nothing
+ *   recent, sinks  >= 0: rows whose position is among the `recent` newest (above the sequence's
+ *           largest position - recent) or below `sinks` are protected
  *   kv bf16 [B][S_max][576], k8 uint8 [B][S_max][128], k_scale fp32 [B][S_max]: the caches whose
  *           rows move (each may be NULL; k8 and k_scale go together)
  *   acc_out, pos_out [B][S_max], kv_len_out [B]: the new state; each may be the input itself

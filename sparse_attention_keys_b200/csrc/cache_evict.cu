@@ -111,7 +111,8 @@ __global__ void __launch_bounds__(kThreads, 1) evict_select_kernel(const EvictPa
       if (src) src[r] = r;
     }
     if (src)
-      for (int r = n + (int)rank * kThreads + tid; r < p.keep; r += p.C * kThreads) src[r] = -1;
+      // in 64 bits: the budget may be any int, the largest included
+      for (int64_t r = (int64_t)n + rank * kThreads + tid; r < p.keep; r += p.C * kThreads) src[r] = -1;
     if (rank == 0 && tid == 0) {
       p.len_out[b] = n;
       moves[0] = 0;

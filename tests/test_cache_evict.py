@@ -228,3 +228,20 @@ def test_ties_across_every_warp_and_part_of_the_state_in_place(B, S, keep):
     assert torch.equal(acc[:, :keep], rows[0]) and torch.equal(pos_out[:, :keep], rows[1])
     assert torch.equal(pos, before) and bool((pos_out[:, keep:] == -7).all())
     assert dsa.dsa_get_device_status() == 0
+
+
+@gpu
+def test_a_budget_of_every_int():
+    """The largest budget there is: nothing to give up, and all of src behind the rows is -1."""
+    keep = (1 << 31) - 1
+    acc, pos, _, _, _ = state(1, 8, seed=2)
+    n = torch.tensor([6], dtype=torch.int32, device="cuda")
+    src = torch.zeros((1, keep), dtype=torch.int32, device="cuda")
+    assert dsa.dsa_cache_evict_workspace_size(1, 8, keep) == 16
+    out = [torch.full_like(acc, -7.0), torch.full_like(pos, -7), torch.empty_like(n)]
+    dsa.dsa_cache_evict(acc, pos, n, keep, acc_out=out[0], pos_out=out[1], kv_len_out=out[2], src=src)
+    assert dsa.dsa_get_device_status() == 0
+    assert out[2].tolist() == [6] and src[0, :6].tolist() == list(range(6))
+    assert torch.equal(out[0][0, :6], acc[0, :6]) and torch.equal(out[1][0, :6], pos[0, :6])
+    assert bool((out[0][0, 6:] == -7.0).all()) and bool((out[1][0, 6:] == -7).all())
+    assert all(bool((c == -1).all()) for c in src[0, 6:].split(1 << 28))
