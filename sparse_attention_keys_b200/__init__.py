@@ -572,6 +572,19 @@ def _dims(t, name, dtype, n):
     return t.shape
 
 
+def _int32(**values):
+    """Refuses what the C ABI's int does not hold: ctypes passes the low 32 bits of a larger integer."""
+    for name, v in values.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError(f"{name} = {v} does not fit into 32 bits")
+
+
+def _shape_bytes(query, *shape):
+    """query(*shape), or 0 (an invalid shape) where a size does not fit the C ABI's int."""
+    shape = [int(n) for n in shape]
+    return int(query(*shape)) if -0x80000000 <= min(shape) and max(shape) <= 0x7fffffff else 0
+
+
 def _scratch(workspace, size, device):
     """The caller's workspace as (tensor, bytes), or a fresh one of `size` bytes."""
     if workspace is None:
@@ -587,6 +600,7 @@ def dsa_rope_freqs(pairs: int, theta: float = 10000.0, factor: float = 1.0, orig
     slows them for long contexts: by YaRN with original_len > 0, all alike with original_len = 0."""
     if int(pairs) < 1:
         raise ValueError("pairs must be at least 1")
+    _int32(pairs=int(pairs), original_len=int(original_len))
     out = torch.empty(int(pairs), dtype=torch.int64)
     _check(_lib.dsa_rope_freqs(_ptr(out), int(pairs), float(theta), float(factor), int(original_len), float(beta_fast),
                                float(beta_slow)), "dsa_rope_freqs")
@@ -628,6 +642,8 @@ def _rope(x, pos, freqs, offset, interleaved, inverse, scale, out, s):
         (rows, dim), heads = shape, 1
     else:
         raise ValueError(f"x must be [rows, heads, dim] or [rows, dim], got {list(shape)}")
+    if heads > 0x7fffffff or dim > 0x7fffffff:
+        _int32(heads=heads, dim=dim)
     (pairs,) = _dims(freqs, "freqs", torch.int64, 1)
     if pairs < 1 or offset < 0 or offset + 2 * pairs > dim:
         raise ValueError(f"features [{offset}, {offset + 2 * pairs}) do not lie in a head of {dim}")
@@ -662,7 +678,7 @@ def _rope(x, pos, freqs, offset, interleaved, inverse, scale, out, s):
 
 def dsa_mla_shared_workspace_size(B: int, T: int, P: int, S_max: int) -> int:
     """Bytes of scratch dsa_mla_shared needs on the current device."""
-    return int(_lib.dsa_mla_shared_workspace_size(int(B), int(T), int(P), int(S_max)))
+    return _shape_bytes(_lib.dsa_mla_shared_workspace_size, B, T, P, S_max)
 
 
 def dsa_mla_shared(q, prefix, kv=None, q_pos=None, kv_len=None, softmax_scale: float = MLA_SOFTMAX_SCALE, out=None,
@@ -752,6 +768,7 @@ def dsa_mla_weights_selected(q, kv, idx, lse, softmax_scale: float = MLA_SOFTMAX
     """dsa_mla_weights for sparse attention: idx i32 [B,T,k] as given to dsa_sparse_mla (-1: unused slot), lse as it
     returned it -> (w fp32 [B,T,ld], acc); w[..., u] is the weight of slot u, ld is k rounded up to 4."""
     k = _dims(idx, "idx", torch.int32, 3)[2]
+    _int32(k=k)
 
     def own(B, T, device):
         return (_arg(idx, "idx", torch.int32, (B, T, k), device),)
@@ -760,7 +777,7 @@ def dsa_mla_weights_selected(q, kv, idx, lse, softmax_scale: float = MLA_SOFTMAX
 
 
 def dsa_cache_evict_workspace_size(B: int, S_max: int, keep: int) -> int:
-    return int(_lib.dsa_cache_evict_workspace_size(int(B), int(S_max), int(keep)))
+    return _shape_bytes(_lib.dsa_cache_evict_workspace_size, B, S_max, keep)
 
 
 def dsa_cache_evict(acc, pos, kv_len, keep: int, recent: int = 0, sinks: int = 0, kv=None, k8=None, k_scale=None,
@@ -771,9 +788,10 @@ def dsa_cache_evict(acc, pos, kv_len, keep: int, recent: int = 0, sinks: int = 0
     place unless acc_out, pos_out, kv_len_out are given. Returns (acc, pos, kv_len, src), src i32 [B,keep] naming the
     row that each kept row came from (-1 behind them)."""
     B, S = _dims(acc, "acc", torch.float32, 2)
-    keep = int(keep)
+    keep, recent, sinks = int(keep), int(recent), int(sinks)
     if keep < 1:
         raise ValueError("keep must be at least 1")
+    _int32(B=B, S=S, keep=keep, recent=recent, sinks=sinks)
     if (k8 is None) != (k_scale is None):
         raise ValueError("k8 and k_scale go together")
     device = acc.device
@@ -791,7 +809,7 @@ def dsa_cache_evict(acc, pos, kv_len, keep: int, recent: int = 0, sinks: int = 0
     def call(s):
         to = torch.empty((B, keep), dtype=torch.int32, device=device) if src is None else src
         ws, size = _scratch(workspace, _lib.dsa_cache_evict_workspace_size(B, S, keep), device)
-        _check(_lib.dsa_cache_evict(acc_ptr, pos_ptr, len_ptr, B, S, keep, int(recent), int(sinks), kv_ptr, k8_ptr, ks_ptr,
+        _check(_lib.dsa_cache_evict(acc_ptr, pos_ptr, len_ptr, B, S, keep, recent, sinks, kv_ptr, k8_ptr, ks_ptr,
                                     acc_out_ptr, pos_out_ptr, len_out_ptr, to.data_ptr(), ws.data_ptr(), size, s),
                "dsa_cache_evict")
         return (acc if acc_out is None else acc_out, pos if pos_out is None else pos_out,
