@@ -8,6 +8,7 @@ the library's CUDA kernels; there is no fallback path. Names follow the C entry 
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -617,13 +618,29 @@ def _rope_strides(t, name, rows, heads, dim):
     return st[0] if rows > 1 else heads * dim, st[1] if heads > 1 else dim
 
 
+def _rope_apart(d, rows, heads, dim, xr, xh, yr, yh):
+    """Whether no element of out, d elements behind x, is one of x's. What the strides do not tell counts as overlapping."""
+    row_x, row_y = (heads - 1) * xh + dim, (heads - 1) * yh + dim
+    if d >= (rows - 1) * xr + row_x or -d >= (rows - 1) * yr + row_y:
+        return True
+    col_x, col_y = (rows - 1) * xr + dim, (rows - 1) * yr + dim
+    # the memory they span meets: they may still be different columns of the same rows, rows of the same heads, or
+    # parts of whatever both have at every `period`
+    steps = [n for n, many in ((xr, rows > 1), (yr, rows > 1), (xh, heads > 1), (yh, heads > 1)) if many]
+    for period, wide_x, wide_y in ((xr if xr == yr else 0, row_x, row_y), (xh if xh == yh else 0, col_x, col_y),
+                                   (math.gcd(*steps), dim, dim)):
+        if period > 0 and d % period >= wide_x and d % period + wide_y <= period:
+            return True
+    return False
+
+
 def dsa_rope(x, pos, freqs, offset: int = 0, interleaved: bool = False, inverse: bool = False, scale: float = 1.0,
              out=None, stream=None):
     """x fp32, bf16 or fp16 [rows, heads, dim] or [rows, dim], features contiguous, rows and heads at any stride;
     pos i32 [rows]; freqs i64 [pairs] from dsa_rope_freqs, on the device. Rotates the features
     [offset, offset + 2 pairs) of each head as pairs (2i, 2i+1) if interleaved, else (i, i + pairs), and copies the
-    others into `out` (new and contiguous by default; out=x rotates in place). inverse=True with the same scale is the
-    gradient with respect to x."""
+    others into `out` (new and contiguous by default; out=x rotates in place; other columns, rows or heads of x's memory
+    are fine, elements of x are not). inverse=True with the same scale is the gradient with respect to x."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _ROPE_DTYPES:
         raise TypeError("x must be a float32, bfloat16 or float16 tensor")
     if not x.is_cuda:
@@ -663,13 +680,8 @@ def _rope(x, pos, freqs, offset, interleaved, inverse, scale, out, s):
         yp = out.data_ptr()
     if rows == 0 or heads == 0:
         return out
-    if xp != yp or xr != yr or xh != yh:
-        size, wide_x, wide_y = x.element_size(), (heads - 1) * xh + dim, (heads - 1) * yh + dim
-        if xp < yp + size * ((rows - 1) * yr + wide_y) and yp < xp + size * ((rows - 1) * xr + wide_x):
-            # the memory they span meets: they may still be different columns of the same rows
-            gap = (yp - xp) // size % xr if xr == yr and xr > 0 else 0
-            if gap < wide_x or gap + wide_y > xr:
-                raise ValueError("out must be x itself or not overlap it")
+    if (xp != yp or xr != yr or xh != yh) and not _rope_apart((yp - xp) // x.element_size(), rows, heads, dim, xr, xh, yr, yh):
+        raise ValueError("out must be x itself or not overlap it")
     flags = (DSA_ROPE_INTERLEAVED if interleaved else 0) | (DSA_ROPE_INVERSE if inverse else 0)
     _check(_lib.dsa_rope(xp, _ROPE_DTYPES[x.dtype], rows, heads, xr, xh, dim, offset, pairs, pos_ptr, freqs_ptr, scale, flags,
                          yp, yr, yh, s), "dsa_rope")
