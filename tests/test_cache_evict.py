@@ -245,3 +245,14 @@ def test_a_budget_of_every_int():
     assert torch.equal(out[0][0, :6], acc[0, :6]) and torch.equal(out[1][0, :6], pos[0, :6])
     assert bool((out[0][0, 6:] == -7.0).all()) and bool((out[1][0, 6:] == -7).all())
     assert all(bool((c == -1).all()) for c in src[0, 6:].split(1 << 28))
+
+
+@gpu
+@pytest.mark.parametrize("S", [131071, 131073])
+def test_at_the_register_capacity(S):
+    """Eight CTAs hold 131072 rows in registers; from one more on every pass reads them again."""
+    acc = torch.rand((1, S), generator=torch.Generator(device="cuda").manual_seed(S), device="cuda")
+    acc = (acc * 1000).floor()
+    pos = torch.arange(S, device="cuda", dtype=torch.int32)[None].contiguous()
+    for n in (S, S - 1):
+        check(acc, pos, [n], 60001, 500, 4, caches=False)

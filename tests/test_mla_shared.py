@@ -261,3 +261,21 @@ def test_own_rows_past_32_bit_offsets():
     kv[:, 201:205] = float("nan")
     out, lse = dsa.dsa_mla_shared(q, prefix, kv, lens[:, None] - 1, lens)
     check(out, lse, q, prefix, kv, lens[:, None] - 1, lens)
+
+
+@gpu
+@pytest.mark.parametrize("B,T,P,S", [(1000, 1, 70, 64), (3, 301, 70, 150), (901, 1, 0, 140), (1, 1601, 130, 20)])
+def test_more_units_than_threads_plan_at_once(B, T, P, S):
+    """Over 768 tokens a thread plans several units, and cuts fall between and inside them; sequences without a row
+    among them, and (without a prefix) whole units that see nothing."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, S + 1, (B,), generator=g)
+    lens[::3] = 0
+    lens[40:60] = 0
+    lens[-1] = S
+    args = make(B, T, P, S, seed=13, lens=lens.cuda())
+    out, lse = dsa.dsa_mla_shared(*args)
+    assert dsa.dsa_get_device_status() == 0
+    check(out, lse, *args)
+    again = dsa.dsa_mla_shared(*args)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])

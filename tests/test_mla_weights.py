@@ -323,3 +323,119 @@ def test_the_whole_loop():
             ref = torch.stack([held[b][s][1] for s in order])
             assert bool(((acc[b, :m].double() - ref).abs() <= 1e-3 * ref + 1e-6).all())
     assert dsa.dsa_get_device_status() == 0
+
+
+@gpu
+def test_prefix_and_own_rows_with_the_lse_of_both():
+    """A prefix that the batch shares is one sequence with every query; with the lse over prefix and own rows the two
+    calls' weights are those of one softmax."""
+    B, T, P, S = 3, 2, 150, 70
+    q, kv, q_pos, kv_len = make(B, T, S, seed=4, lens=[S, 0, 33])
+    prefix = make(1, 1, P, seed=5)[1]
+    _, lse = dsa.dsa_mla_shared(q, prefix[0], kv, q_pos, kv_len)
+    own, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len)
+    everywhere = torch.full((1, B * T), P - 1, dtype=torch.int32, device="cuda")
+    before = torch.rand((1, P), device="cuda")
+    shared, acc = dsa.dsa_mla_weights(q.view(1, B * T, 128, 576), prefix, lse.view(1, B * T, 128), everywhere,
+                                      torch.tensor([P], dtype=torch.int32, device="cuda"), acc=before.clone())
+    assert dsa.dsa_get_device_status() == 0
+    rows = [[torch.arange(visible(q_pos, kv_len, S, b, t), device="cuda") for t in range(T)] for b in range(B)]
+    ref = reference(q, kv, lse, rows)
+    total, slack = before[0].double(), torch.zeros(P, dtype=torch.float64, device="cuda")
+    every = [[torch.arange(P, device="cuda")]]
+    for b in range(B):
+        for t in range(T):
+            i = b * T + t
+            want, tol = reference(q[b:b + 1, t:t + 1], prefix, lse[b:b + 1, t:t + 1], every)[0][0]
+            close(shared[0, i, :P], want, tol)
+            close(own[b, t, :len(rows[b][t])], *ref[b][t])
+            # one softmax over both, 128 heads of it; its lse is off by the scores' error d (within 2 d of the tolerance)
+            both, room = want.sum() + ref[b][t][0].sum(), tol.sum() + ref[b][t][1].sum()
+            assert abs(float(both) - 128) <= 2 * float(room)
+            total += want
+            slack += tol
+    close(acc[0], total, slack + (B * T + 1) * 2.0 ** -24 * total)
+
+
+@gpu
+def test_the_sparse_loop():
+    """As the path decodes: the indexer's keys enter their cache, dsa_index_topk selects, dsa_sparse_mla attends, its lse
+    gives the selected rows' weights, and a full cache is evicted with the indexer's codes and scales. The rows' order
+    changes nothing: the same selection, as positions, as from a cache in the order of positions, and the attention is
+    that of the selected rows in 64 bits."""
+    B, S, keep, k, start, steps = 3, 96, 64, 24, 80, 60
+    g = torch.Generator(device="cuda").manual_seed(17)
+
+    def normal(*s):
+        return torch.randn(s, generator=g, device="cuda")
+
+    table = dsa.dsa_rope_table(1024).cuda()
+    k8, ks = torch.zeros((B, S, 128), dtype=torch.uint8, device="cuda"), torch.zeros((B, S), device="cuda")
+    kv = torch.zeros((B, S, 576), dtype=torch.bfloat16, device="cuda")
+    pos, acc = torch.zeros((B, S), dtype=torch.int32, device="cuda"), torch.zeros((B, S), device="cuda")
+    kv_len = torch.zeros(B, dtype=torch.int32, device="cuda")
+    first = torch.arange(B, device="cuda") * S
+    # every key at its position, never moved: what the evicted cache is compared with
+    n_all = start + steps
+    all8, all_s = torch.zeros((B, n_all, 128), dtype=torch.uint8, device="cuda"), torch.zeros((B, n_all), device="cuda")
+    all_kv = torch.zeros((B, n_all, 576), dtype=torch.bfloat16, device="cuda")
+    evictions = 0
+
+    def append(at):
+        """One token per sequence, at position `at`."""
+        n = int(kv_len[0])
+        p = torch.full((B,), at, dtype=torch.int32, device="cuda")
+        key, row = normal(B, 128), normal(B, 576).bfloat16()
+        dsa.dsa_index_keys(key, p, table, out_fp8=k8, out_scale=ks, dst_row=first + n)
+        dsa.dsa_index_keys(key, p, table, out_fp8=all8, out_scale=all_s, dst_row=torch.arange(B, device="cuda") * n_all + at)
+        kv[:, n], all_kv[:, at], pos[:, n], acc[:, n] = row, row, at, 0.0
+        kv_len.add_(1)
+
+    for at in range(start):
+        append(at)
+    for step in range(steps):
+        at = start + step
+        append(at)
+        n = int(kv_len[0])
+        p = torch.full((B,), at, dtype=torch.int32, device="cuda")
+        q8, qs = dsa.dsa_index_keys(normal(B, 64, 128), p, table)
+        q8, qs, w = q8[:, None].contiguous(), qs[:, None].contiguous(), normal(B, 1, 64)
+        q_pos = (kv_len[:, None] - 1).contiguous()
+        idx = dsa.dsa_index_topk(q8, qs, w, k8, ks, q_pos, kv_len, k)
+        picked = pos.gather(1, idx[:, 0].long()).sort(1).values
+        # the same rows in the order of their positions
+        order = pos[:, :n].sort(1).values.long()
+        bi = torch.arange(B, device="cuda")[:, None]
+        sorted8, sorted_s = all8[bi, order].contiguous(), all_s[bi, order].contiguous()
+        ref = dsa.dsa_index_topk(q8, qs, w, sorted8, sorted_s, q_pos, kv_len, k)
+        assert torch.equal(picked.long(), order.gather(1, ref[:, 0].long()).sort(1).values)
+        q = normal(B, 1, 128, 576).bfloat16()
+        out, lse = dsa.dsa_sparse_mla(q, kv, idx)
+        before = acc.clone()
+        weights, _ = dsa.dsa_mla_weights_selected(q, kv, idx, lse, acc=acc)
+        rows = [[idx[b, 0].long()] for b in range(B)]
+        ref_w = reference(q, kv, lse, rows)
+        for b in range(B):
+            keys = all_kv[b, pos[b, idx[b, 0].long()].long()].double()
+            pr = torch.softmax(SCALE * q[b, 0].double() @ keys.t(), -1)
+            # bf16 weights and output: 2^-8 each, with room for the scores' 2^-9
+            assert bool(((out[b, 0].double() - pr @ keys[:, :512]).abs() <= 2.0 ** -6 * (pr @ keys[:, :512].abs())).all())
+            close(weights[b, 0, :k], *ref_w[b][0])
+            want = before[b].double().index_add(0, rows[b][0], ref_w[b][0][0])
+            room = torch.zeros_like(want).index_add(0, rows[b][0], ref_w[b][0][1])
+            close(acc[b], want, room + 2.0 ** -23 * want)
+        if n == S:
+            held = [dict(zip(pos[b].tolist(), acc[b].tolist())) for b in range(B)]
+            dsa.dsa_cache_evict(acc, pos, kv_len, keep, recent=8, sinks=2, kv=kv, k8=k8, k_scale=ks)
+            evictions += 1
+            assert kv_len.tolist() == [keep] * B
+            for b in range(B):
+                at_row = pos[b, :keep].long()
+                ranked = sorted(held[b], key=lambda s: (not (s > at - 8 or s < 2), -held[b][s]))
+                cut = held[b][ranked[keep - 1]]
+                for s in set(at_row.tolist()) ^ set(ranked[:keep]):  # positions of equal weight may stand for one another
+                    assert held[b][s] == cut
+                assert torch.equal(k8[b, :keep], all8[b, at_row]) and torch.equal(ks[b, :keep], all_s[b, at_row])
+                assert torch.equal(kv[b, :keep], all_kv[b, at_row])
+                assert acc[b, :keep].tolist() == [held[b][s] for s in at_row.tolist()]
+    assert evictions == 2 and dsa.dsa_get_device_status() == 0
