@@ -659,7 +659,7 @@ def _rope(x, pos, freqs, offset, interleaved, inverse, scale, out, s):
         (rows, dim), heads = shape, 1
     else:
         raise ValueError(f"x must be [rows, heads, dim] or [rows, dim], got {list(shape)}")
-    if heads > 0x7fffffff or dim > 0x7fffffff:
+    if (heads | dim) >> 31:
         _int32(heads=heads, dim=dim)
     (pairs,) = _dims(freqs, "freqs", torch.int64, 1)
     if pairs < 1 or offset < 0 or offset + 2 * pairs > dim:
@@ -803,7 +803,8 @@ def dsa_cache_evict(acc, pos, kv_len, keep: int, recent: int = 0, sinks: int = 0
     keep, recent, sinks = int(keep), int(recent), int(sinks)
     if keep < 1:
         raise ValueError("keep must be at least 1")
-    _int32(B=B, S=S, keep=keep, recent=recent, sinks=sinks)
+    if (B | S | keep | recent | sinks) >> 31:                    # one of them negative, or wide
+        _int32(B=B, S=S, keep=keep, recent=recent, sinks=sinks)
     if (k8 is None) != (k_scale is None):
         raise ValueError("k8 and k_scale go together")
     device = acc.device
