@@ -13,12 +13,17 @@
 // share of it 6300 cycles, and the ring's 144 KB cover its latency (48 to 50 us for 64 queries over 2048 to
 // 4096 rows each, 4.9 TB/s; with 128 KB in slots of 128 features, a tenth of them empty, 51 us).
 //
-// A tile's contraction is cut into three parts of 192 features, a slot and an accumulator of 128 columns each, that
-// are added in registers. The exponential turns an absolute error of the score into a relative one of the
-// weight, and the tensor core's rounding of the running fp32 sum, 36 times over 576 features, was what the
-// weights' error came from: 6.7e-6 of them with one accumulator, 2.1e-6 with three (fp32 matrix products
-// leave 2e-6). The parts take the four accumulators of TMEM in turn, so that the first of a tile is
-// computed while the last one's are read.
+// A tile's contraction is cut into parts that are added in registers, an accumulator of 128 columns each. The
+// exponential turns an absolute error of the score into a relative one of the weight, and the tensor core cuts off
+// its running fp32 sum, 36 times over 576 features, so the error grows with the length of a part: one part left 6.7e-6
+// in the weights, three (192 features, a slot each) leave 2.1e-6 over 2048 to 4096 keys, where fp32 matrix products
+// leave 2.0e-6. Over fewer keys the heaviest scores are smaller and so are the roundings that both forms share: over
+// 64 to 200 keys three parts left 1.1e-6 to 1.4e-6 against 0.5e-6 to 0.9e-6. Queries of at most kFineKeys keys
+// therefore get six parts (96 features, two per slot), which leave 0.7e-6 there and 1.0e-6 against 1.5e-6 over 1024
+// keys; beyond, three are at most 1.3 times as far off as fp32 products. Six everywhere cost the long prompt
+// chunks a third of their speed (250 queries over 4050 rows: 165 instead of 126 us), and the short
+// queries a twentieth (64 over about 1000 rows: 36.9 instead of 34.8 us). The parts take the four accumulators
+// of TMEM in turn, so that the next ones are computed while one is read.
 //
 // Selected rows are gathered by four warps with 16-byte cp.async into the swizzled operand layout,
 // 384 bytes of each row per slot (64 queries of 2048 rows: 45 us, 48 with 256 bytes at a time, 58 with 128, since
@@ -27,6 +32,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kernels.h"
 #include "pair.cuh"
@@ -40,7 +46,8 @@ constexpr int kRows = 128;                         // keys of a tile on each CTA
 constexpr int kTile = 2 * kRows;
 constexpr int kQBlock = 64 * 128;                  // 8 KB: 64 features of this CTA's 64 heads
 constexpr int kBlock = kRows * 128;                // 16 KB: 64 features of 128 keys
-constexpr int kParts = 3;                          // parts of a contraction, 192 features each: a ring slot
+constexpr int kParts = 3;                          // ring slots of a tile, 192 features each
+constexpr int kFineKeys = 1024;                    // queries of at most as many keys get two parts per slot, others one
 constexpr int kSlot = 3 * kBlock;                  // 48 KB
 constexpr int kSlots = 3;
 constexpr int kAccs = 4;                           // accumulators of 128 columns, taken by the parts in turn
@@ -281,34 +288,41 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
       int slot = 0, run = 0;
       uint32_t ph = 0, i = 0;               // parts issued
       bool ok = true;
-      for (; ok && r.left > 0; r.next(p), ++run) {
-        if (!mbar_wait(q_full, run & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_Q)) break;
-        tc_fence_after();
-        const int tiles = r.t1 - r.t0;
-        for (int t = 0; ok && t < tiles; ++t) {
+      // the tiles of a run, a slot's 12 MMAs into one accumulator (PER = 1) or six each into two
+      auto tiles = [&](auto per) {
+        constexpr int PER = decltype(per)::value, kSteps = 12 / PER;
+        for (int t = r.t0; ok && t < r.t1; ++t) {
 #pragma unroll
-          for (int part = 0; part < kParts; ++part) {
+          for (int part = 0; part < kParts * PER; ++part) {
             if (!ok || !mbar_wait(&acc_empty[i & 3], ((i >> 2) + 1) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC) ||
-                !mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL)) {
+                (part % PER == 0 && !mbar_wait(&full[slot], ph, &abort_flag, p.status, DSA_SITE_WEIGHTS_FULL))) {
               ok = false;
               break;
             }
-            if (SELECTED) cluster_fence();                     // both CTAs' threads wrote this slot
+            if (SELECTED && part % PER == 0) cluster_fence();  // both CTAs' threads wrote this slot
             tc_fence_after();
-            const uint64_t a = k_desc + (uint64_t)(slot * (kSlot >> 4)), b = q_desc + (uint64_t)(3 * part * (kQBlock >> 4));
+            const uint64_t a = k_desc + (uint64_t)(slot * (kSlot >> 4)), b = q_desc + (uint64_t)(3 * (part / PER) * (kQBlock >> 4));
 #pragma unroll
-            for (int k = 0; k < 12; ++k)
+            for (int j = 0; j < kSteps; ++j) {
+              const int k = part % PER * kSteps + j;
               pair_mma_ss((i & 3) * kHeads, a + 2 * (k & 3) + (k >> 2) * (kBlock >> 4),
-                          b + 2 * (k & 3) + (k >> 2) * (kQBlock >> 4), idesc, k > 0);
-            pair_commit(&empty[slot], 3);
+                          b + 2 * (k & 3) + (k >> 2) * (kQBlock >> 4), idesc, j > 0);
+            }
+            if (part % PER == PER - 1) pair_commit(&empty[slot], 3);
             pair_commit(&acc_full[i & 3], 3);
             ++i;
-            if (++slot == kSlots) {
+            if (part % PER == PER - 1 && ++slot == kSlots) {
               slot = 0;
               ph ^= 1;
             }
           }
         }
+      };
+      for (; ok && r.left > 0; r.next(p), ++run) {
+        if (!mbar_wait(q_full, run & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_Q)) break;
+        tc_fence_after();
+        if (r.keys <= kFineKeys) tiles(std::integral_constant<int, 2>());
+        else tiles(std::integral_constant<int, 1>());
         if (ok) pair_commit(q_empty, 3);
       }
     }
@@ -395,6 +409,7 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
       __syncwarp();
       *reinterpret_cast<float2*>(ls + 2 * lane) = make_float2(l2.x * kLog2e, l2.y * kLog2e);
       __syncwarp();
+      const bool fine = r.keys <= kFineKeys;
       for (int t = r.t0; ok && t < r.t1; ++t, ++g) {
         const int u = t * kTile + rank * kRows + key;
         bool take = u < r.keys;
@@ -408,10 +423,9 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
         const bool add = half == 0 && take && p.T == 1 && p.acc_out != nullptr;
         const float before = !SELECTED && add ? p.acc[r.tok * p.S_max + row] : 0.f;
         float z[64];
-#pragma unroll
-        for (int part = 0; part < kParts; ++part) {
+        auto read = [&](bool first) {                          // the next part's 64 scores
           ok = ok && __all_sync(0xffffffffu, mbar_wait(&acc_full[i & 3], (i >> 2) & 1, &abort_flag, p.status, DSA_SITE_WEIGHTS_ACC));
-          if (!ok) break;
+          if (!ok) return;
           tc_fence_after();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -420,13 +434,19 @@ __global__ void __launch_bounds__(SELECTED ? 512 : 384, 1)
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              z[32 * c + j] = part == 0 ? __uint_as_float(x[j]) : z[32 * c + j] + __uint_as_float(x[j]);
+              z[32 * c + j] = first ? __uint_as_float(x[j]) : z[32 * c + j] + __uint_as_float(x[j]);
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(cluster_addr(&acc_empty[i & 3], 0));
           ++i;
-        }
+        };
+        read(true);
+#pragma unroll
+        for (int part = 1; part < kParts; ++part) read(false);
+        if (fine)
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) read(false);
         if (!ok) break;
         float s4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

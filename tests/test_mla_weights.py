@@ -439,3 +439,58 @@ def test_the_sparse_loop():
                 assert torch.equal(kv[b, :keep], all_kv[b, at_row])
                 assert acc[b, :keep].tolist() == [held[b][s] for s in at_row.tolist()]
     assert evictions == 2 and dsa.dsa_get_device_status() == 0
+
+
+def relative(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@gpu
+@pytest.mark.parametrize("B,T,S,n,k", [
+    (8, 1, 65, 65, 0), (8, 1, 100, 100, 0), (8, 1, 190, 190, 0), (8, 1, 600, 600, 0), (8, 1, 5000, 100, 0), (2, 7, 120, 120, 0),
+    (4, 1, 1024, 1024, 0), (4, 1, 1025, 1025, 0), (2, 1, 9000, 9000, 0), (8, 1, 5000, 5000, 67), (8, 1, 5000, 5000, 140),
+    (2, 3, 3000, 3000, 130), (4, 1, 9000, 9000, 1024), (4, 1, 9000, 9000, 1500)])
+def test_as_exact_as_fp32_products(B, T, S, n, k):
+    """The weights' error in the 2-norm is that of the scores. With fp32 products and sums, each rounded to nearest, a
+    score of size |z| <= 16 is off by its own last roundings (scale and difference: 2^-24 |z| each, about 5e-7 where the
+    heaviest weights lie) and by the sum's; that form is computed here, and the kernel stays within half more of it, or
+    within 1e-6, about 16 * 2^-24. n rows of S are visible."""
+    q, kv, q_pos, kv_len = make(B, T, S, seed=S + k, lens=[n] * B)
+    q_pos.fill_(n - 1)
+    rows = kv[:, None, :n].expand(B, T, n, 576)
+    if k:
+        g = torch.Generator(device="cuda").manual_seed(k)
+        idx = torch.rand((B, T, S), generator=g, device="cuda").topk(k, -1).indices.sort(-1).values.to(torch.int32).contiguous()
+        rows = kv[torch.arange(B, device="cuda")[:, None, None], idx.long()]
+    exact = SCALE * torch.matmul(q.double(), rows.double().transpose(-1, -2))
+    lse = torch.logsumexp(exact, -1).float()
+    want = torch.exp(exact - lse.double()[..., None]).sum(2)
+    plain = torch.exp(SCALE * torch.matmul(q.float(), rows.float().transpose(-1, -2)) - lse[..., None]).sum(2)
+    if k:
+        w, _ = dsa.dsa_mla_weights_selected(q, kv, idx, lse)
+    else:
+        w, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len)
+    assert dsa.dsa_get_device_status() == 0
+    got, base = relative(w[..., :want.shape[2]], want), relative(plain, want)
+    assert got <= max(1e-6, 1.5 * base), (got, base)
+
+
+@gpu
+def test_queries_on_both_sides_of_the_border():
+    """Queries of 1023 to 1026 visible rows in one call, then short and long ones in turn: what a query gets depends on
+    its own rows alone."""
+    S = 1400
+    q, kv, _, kv_len = make(1, 12, S, seed=31, lens=[S])
+    seen = [1023, 1024, 1025, 1026, 5, 1400, 256, 1025, 1, 1300, 1024, 1399]
+    q_pos = torch.tensor([[n - 1 for n in seen]], dtype=torch.int32, device="cuda")
+    rows = [[torch.arange(n, device="cuda") for n in seen]]
+    lse = lse_of(q, kv, rows)
+    w, _ = dsa.dsa_mla_weights(q, kv, lse, q_pos, kv_len)
+    ref = reference(q, kv, lse, rows)
+    for t, n in enumerate(seen):
+        close(w[0, t, :n], *ref[0][t])
+        assert bool((w[0, t, n:S] == 0).all())
+        alone, _ = dsa.dsa_mla_weights(q[:, t:t + 1].contiguous(), kv, lse[:, t:t + 1].contiguous(),
+                                       torch.tensor([[n - 1]], dtype=torch.int32, device="cuda"), kv_len)
+        assert torch.equal(alone[0, 0, :S], w[0, t, :S])
+    assert dsa.dsa_get_device_status() == 0
