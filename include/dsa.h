@@ -361,7 +361,8 @@ DSA_API size_t dsa_sparse_mla_heads_workspace_size(int B, int T, int k, int head
  * buffer `freqs`, as fractions of a turn per position in units of 2^-64:
  * f_i = theta^(-i / pairs) radians, for factor > 1 slowed for long contexts: with original_len > 0
  * the YaRN blend (pairs that turn more than beta_fast times in original_len positions keep f_i,
- * those below beta_slow get f_i / factor, linear between, the correction range rounded outwards),
+ * those below beta_slow get f_i / factor, linear between, the correction range rounded outwards and
+ * starting at pair 0 at the earliest, which so keeps its frequency at any original_len),
  * with original_len = 0 every pair gets f_i / factor. theta 1e4, factor 40, original_len 4096,
  * beta 32 and 1 give the frequencies of dsa_rope_table.
  * DSA_ERR_INVALID_ARG unless freqs is given, 1 <= pairs <= 2048, theta > 1, factor >= 1,
@@ -385,9 +386,11 @@ DSA_API int dsa_rope_freqs(uint64_t* freqs, int pairs, double theta, double fact
  *            (the indexer's); DSA_ROPE_INVERSE: turn by -pos, which is the gradient: with g the
  *            gradient of out, dsa_rope(g, ..., the same scale, DSA_ROPE_INVERSE) is that of x
  *   scale    a finite factor on the rotated features (YaRN's attention factor), 1 for none
- * pos * f is exact modulo a turn at any position; sine and cosine are fp32, and the result is
- * rounded once to dtype. x and out need only the alignment of their elements (16-byte aligned rows
- * run faster), pos 4 bytes and freqs 8. 1 <= heads <= 4096, 1 <= dim <= 4096, rows = 0 does nothing.
+ * pos * f is exact modulo a turn at any position. The arithmetic is fp32 (the angle, its sine and
+ * cosine, the products and their sum are each rounded): the pair of (u, v) is within 2^-21 * |scale| *
+ * (|u| + |v|) and is then rounded to dtype. x and out need only the alignment of their elements
+ * (16-byte aligned rows run faster), pos 4 bytes and freqs 8. 1 <= heads <= 4096, 1 <= dim <= 4096,
+ * rows = 0 does nothing.
  */
 DSA_API int dsa_rope(const void* x, int dtype, int64_t rows, int heads, int64_t x_row_stride, int64_t x_head_stride,
                      int dim, int offset, int pairs, const int32_t* pos, const uint64_t* freqs, float scale,
@@ -407,6 +410,9 @@ DSA_API int dsa_rope(const void* x, int dtype, int64_t rows, int heads, int64_t 
  *   workspace / ws_bytes: at least dsa_mla_shared_workspace_size(B, T, P, S_max) bytes; holds
  *           nothing between calls, and must not be shared by calls that overlap on the GPU
  * z = softmax_scale * q . key over the 576 features of the visible rows, out = softmax(z) . key[0:512].
+ * Scores, maxima, row sums and outputs are held in fp32. As in dsa_sparse_mla the probabilities are
+ * rounded to bf16 for their product with the values (the row sum is taken before that), and out to
+ * bf16: |error| <= 2^-8 * sum p |v| + 2^-8 * |out| beside that of the fp32 scores; lse is fp32's.
  * A query that sees no row gets zeros and lse = -inf. Own rows that a query does not see may hold
  * anything, NaN included.
  * P + S_max >= 1; B * T <= 2^23; P and S_max at most DSA_MAX_POS; pointers 16-byte aligned.
@@ -431,6 +437,9 @@ DSA_API size_t dsa_mla_shared_workspace_size(int B, int T, int P, int S_max);
  *           (entries from S_max to ld are left as they were)
  *   acc, acc_out  fp32 [B][S_max], or both NULL: acc_out[b][s] = acc[b][s] + sum over t of w[b][t][s],
  *           added in a fixed order (the same bits every time); acc_out may be acc
+ * Contractions are fp32 sums in three parts, six for queries of at most 1024 keys, that are added in fp32;
+ * the exponential is good to 2^-21. A weight's relative error is that of its scores: 0.7e-6 over 100
+ * keys of N(0,1) and 2.1e-6 over 4000, about as fp32 matrix products leave it.
  * Rows that a query does not see may hold anything. B, T, S_max >= 1; B <= 65535; B * T <= 2^23;
  * S_max at most DSA_MAX_POS; pointers 16-byte aligned.
  */

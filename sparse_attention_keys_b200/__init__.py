@@ -777,8 +777,9 @@ def dsa_mla_weights(q, kv, lse, q_pos, kv_len, softmax_scale: float = MLA_SOFTMA
 
 def dsa_mla_weights_selected(q, kv, idx, lse, softmax_scale: float = MLA_SOFTMAX_SCALE, acc=None, acc_out=None, w=None,
                              stream=None):
-    """dsa_mla_weights for sparse attention: idx i32 [B,T,k] as given to dsa_sparse_mla (-1: unused slot), lse as it
-    returned it -> (w fp32 [B,T,ld], acc); w[..., u] is the weight of slot u, ld is k rounded up to 4."""
+    """dsa_mla_weights for sparse attention: idx i32 [B,T,k] as given to dsa_sparse_mla (-1: unused slot; the others
+    distinct within a query), lse as it returned it -> (w fp32 [B,T,ld], acc); w[..., u] is the weight of slot u, ld is
+    k rounded up to 4."""
     k = _dims(idx, "idx", torch.int32, 3)[2]
     _int32(k=k)
 
